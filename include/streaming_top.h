@@ -60,11 +60,12 @@ typedef enum si_status {
 typedef enum si_dtype {
   SI_DTYPE_BF16 = 0,      /* q, kc are bf16 */
   SI_DTYPE_FP8_E4M3 = 1,  /* q, kc are OCP fp8 e4m3 codes with per-row fp32 scales */
-  SI_DTYPE_MXFP4_KEYS = 2 /* q is bf16; kc is MXFP4 (the 4-bit indexer keys of the V4.1-Flash
+  SI_DTYPE_MXFP4_KEYS = 2, /* q is bf16; kc is MXFP4 (the 4-bit indexer keys of the V4.1-Flash
                              deployment notes, "two-level sparse attention"): OCP Microscaling
                              FP4, E2M1 codes [B,T,D/2] bytes -- value d in the low nibble of byte
                              d/2 when d is even, the high nibble when odd -- with one E8M0 scale
                              per 32 values along D in kc_mx_scale [B,T,D/32] */
+  SI_DTYPE_FP16 = 3       /* the K/V-cache and window attention calls only: IEEE half */
 } si_dtype;
 
 /* Options of si_indexer_topk_ex.  Zero-initialise, then set what you need. */
@@ -274,6 +275,150 @@ SI_API size_t si_two_stage_workspace_size(int B, int S, int T, int block, int n_
 SI_API si_status si_sparse_attention(const void* q, const void* kv, const int32_t* idx, int B, int S, int T,
                                      int H, int Dk, int Dv, int k, float scale, void* out, float* lse,
                                      void* stream, const si_options* opt);
+
+/* ------------------------------------------------------------------------
+ * The raw-token branch: attention through a sliding window with sinks, and the
+ * paged 8-bit K/V cache that serves it.
+ *
+ * The layer that the indexer belongs to has a second branch that attends over
+ * raw tokens in a sliding window (the V4.1 page, "two-level sparse attention",
+ * level one, 128 tokens).  Its prompts go through si_window_attention; while
+ * serving, its keys and values live in pages of e4m3 codes that
+ * si_cache_append fills and si_cache_attention reads, and whole sequences are
+ * given room, forked, freed and moved together by the page calls.
+ *
+ * Visibility, shared by both attentions: the query at position p sees key j
+ * iff 0 <= j <= p and (window == 0 or j > p - window or j < n_sink).  The
+ * first n_sink tokens (the sinks) so stay visible from everywhere.
+ *
+ * All calls: device pointers owned by the caller; asynchronous on `stream`;
+ * argument errors return synchronously and enqueue nothing.  They are forward
+ * passes, as every call of this library.
+ * --------------------------------------------------------------------- */
+
+/* A paged K/V cache.  A page holds `page` consecutive tokens of one sequence
+ * for every key/value head, as OCP e4m3 codes with one fp32 scale per page and
+ * head: value = code * scale.  scale >= 0 and finite (0: all values are 0). */
+typedef struct si_cache {
+  void* k_pages;   /* [n_pages, H_kv, page, D] e4m3 codes, 16-byte aligned */
+  void* v_pages;   /* the same for the values */
+  float* k_scale;  /* [n_pages, H_kv] fp32 */
+  float* v_scale;
+  int n_pages;     /* n_pages * H_kv * page < 2^31 */
+  int H_kv;
+  int page;        /* 16, 32, 64 or 128 */
+  int D;           /* 64 or 128 */
+} si_cache;
+
+/*
+ * Appends rows to the sequences of a cache: row i < n_new[b] of k, v
+ * [B, L, H_kv, D] (dtype SI_DTYPE_BF16 or SI_DTYPE_FP16) becomes token
+ * lens[b] + i of sequence b, in page table[b, (lens[b] + i) / page].
+ * table [B, max_pages] int32, lens [B] int32 (tokens held before; not
+ * changed), n_new [B] int32 or NULL (= L for all; values outside [0, L] are
+ * clamped).  Rows whose page is missing (an entry outside [0, n_pages), or
+ * past max_pages) or whose position is negative are dropped.
+ *   The scale of a touched page and head is the least power of two s with
+ * amax <= 448 s, amax over the finite magnitudes of its new rows (0 if they
+ * are all 0); with older tokens in the page (tokens before lens[b]) it is
+ * max(s, old scale), and if that grew, their codes are re-encoded from
+ * code * old scale.  code = e4m3(value / scale), round to nearest even,
+ * saturating at +-448; NaN stays NaN.  Slots behind the new rows are left as
+ * they were.  No page may be touched by two sequences of a call (a forked
+ * sequence has its own last page: si_cache_fork).
+ */
+SI_API si_status si_cache_append(const si_cache* cache, const void* k, const void* v, const int32_t* table,
+                                 const int32_t* lens, const int32_t* n_new, int B, int L, int max_pages,
+                                 int dtype, void* stream);
+
+/*
+ * Attention of the last L tokens of each sequence over its cache (decode: L =
+ * 1; drafted tokens: a few): query i of q [B, L, H, D] is at position
+ * lens[b] - L + i, where lens[b] counts the tokens in the cache, the queries'
+ * own among them; head h reads key/value head h / (H / H_kv).
+ *   out [B, L, H, D] of q's dtype: sum_j softmax_j(scale q.k_j) v_j
+ *   lse [B, L, H] fp32 (written; may be NULL): ln sum_j exp(scale q.k_j)
+ * over the visible tokens.  A query that sees nothing (a negative position
+ * among them) gets out = 0 and lse = -inf.  Tokens of pages that are missing
+ * (entries outside [0, n_pages)) are not visible; lens[b] beyond max_pages *
+ * page is read as that.  What lies in slots that nobody sees (NaN, stale
+ * codes) has no effect.  scale 0 = 1/sqrt(D).  dtype SI_DTYPE_BF16 or
+ * SI_DTYPE_FP16.  H a multiple of H_kv, H / H_kv <= 128; L >= 1; window and
+ * n_sink >= 0.  Scratch for partial results is taken from opt->workspace when
+ * it is given and large enough (si_cache_attention_workspace_size()), else
+ * allocated on `stream`; opt->device_status is honoured, opt may be NULL.
+ */
+SI_API si_status si_cache_attention(const void* q, const si_cache* cache, const int32_t* table,
+                                    const int32_t* lens, int B, int L, int H, int max_pages, int window,
+                                    int n_sink, float scale, int dtype, void* out, float* lse, void* stream,
+                                    const si_options* opt);
+
+/* Scratch bytes that suffice for any si_cache_attention call with D on the current device. */
+SI_API size_t si_cache_attention_workspace_size(int D);
+
+/*
+ * Attention of whole prompts through the window: q [B, S, H, D], k and v
+ * [B, S, H_kv, D] of one dtype (SI_DTYPE_BF16 or SI_DTYPE_FP16), query i of a
+ * sequence at position i; lens [B] int32 or NULL (= S for all; clamped to
+ * [0, S]) gives the tokens that are there, the rest is padding: padded keys
+ * are never visible, whatever they hold, and padded queries get out = 0 and
+ * lse = -inf.  window >= 1 (S or more: plain causal attention), n_sink >= 0;
+ * out and lse (may be NULL) as si_cache_attention's, [B, S, H, D] and
+ * [B, S, H].  D 64 or 128, H a multiple of H_kv, H / H_kv <= 128,
+ * B * S * H < 2^31.  16-byte aligned.  opt may be NULL (device_status is honoured).
+ */
+SI_API si_status si_window_attention(const void* q, const void* k, const void* v, const int32_t* lens, int B,
+                                     int S, int H, int H_kv, int D, int window, int n_sink, float scale,
+                                     int dtype, void* out, float* lse, void* stream, const si_options* opt);
+
+/* Page management.  table [n_seq, max_pages] int32 (-1 = no page), lens
+ * [n_seq] int32 and refs [n_pages] int32, the number of table entries that
+ * hold a page: 0 = free.  A sequence's pages are the leading entries of its
+ * row that lie in [0, n_pages).  New pages are the lowest free ones, given
+ * out in order, so that results do not depend on timing.  n_seq and n <=
+ * 8192, else SI_ERR_UNSUPPORTED.  status words: 0 done, 1 too few free pages,
+ * 2 not possible (each call says when); a row with a status other than 0 is
+ * left as it was.  Calls that work on the same state belong on one stream. */
+
+/*
+ * Gives every sequence b the pages for n_new[b] more tokens: its row then
+ * covers lens[b] + n_new[b] tokens (n_new <= 0: nothing to do).  Rows are
+ * served in order; from the first on whose need, added to those before it,
+ * exceeds the free pages, rows that need any get status 1.  Status 2: the
+ * row would need more than max_pages.  lens is not changed.  status [n_seq].
+ */
+SI_API si_status si_cache_reserve(const si_cache* cache, int32_t* table, const int32_t* lens, int32_t* refs,
+                                  const int32_t* n_new, int n_seq, int max_pages, int32_t* status,
+                                  void* stream);
+
+/*
+ * Forks sequences: row dst[i] becomes a copy of row src[i] as it was before
+ * the call, i < n.  share != 0: full pages are shared (their refs grow) and
+ * only a last, partly filled page is copied, so that both can be appended to;
+ * share == 0: every page is copied.  Pages that src holds beyond lens are not
+ * taken over.  Status 2: an index outside [0, n_seq), dst[i] not empty (lens
+ * 0 and no page), or the dst of an earlier pair; status 1 as in
+ * si_cache_reserve, by pairs.  status [n].
+ */
+SI_API si_status si_cache_fork(const si_cache* cache, int32_t* table, int32_t* lens, int32_t* refs,
+                               const int32_t* src, const int32_t* dst, int n, int n_seq, int max_pages,
+                               int share, int32_t* status, void* stream);
+
+/* Frees the sequences rows[i], i < n: their pages' refs fall, their entries
+ * become -1 and their lens 0.  Rows outside [0, n_seq) are ignored, a row
+ * named twice is freed once. */
+SI_API si_status si_cache_free(int32_t* table, int32_t* lens, int32_t* refs, const int32_t* rows, int n,
+                               int n_seq, int max_pages, int n_pages, void* stream);
+
+/*
+ * Moves the pages in use together: with U pages in use (refs > 0), the i-th
+ * used page at or above U moves into the i-th free page below U, and table
+ * and refs follow.  used [1] int32 (written): U.  moved [n_pages] int32
+ * (written): the new place of each page that was in use, -1 for the others.
+ * The old places keep their bytes.
+ */
+SI_API si_status si_cache_compact(const si_cache* cache, int32_t* table, int32_t* refs, int n_seq,
+                                  int max_pages, int32_t* used, int32_t* moved, void* stream);
 
 /*
  * Decodes MXFP4 rows to bf16: codes [rows, D/2] bytes (value d in the low

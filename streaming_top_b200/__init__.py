@@ -28,7 +28,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 SI_OK, SI_ERR_INVALID_ARGUMENT, SI_ERR_UNSUPPORTED, SI_ERR_OUT_OF_MEMORY, SI_ERR_CUDA, SI_ERR_TIMEOUT = range(6)
-SI_DTYPE_BF16, SI_DTYPE_FP8_E4M3, SI_DTYPE_MXFP4_KEYS = 0, 1, 2
+SI_DTYPE_BF16, SI_DTYPE_FP8_E4M3, SI_DTYPE_MXFP4_KEYS, SI_DTYPE_FP16 = 0, 1, 2, 3
 
 _vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 
@@ -37,6 +37,12 @@ class Options(ctypes.Structure):
     _fields_ = [("dtype", _i), ("q_scale", _vp), ("kc_scale", _vp), ("query_chunk", _i),
                 ("key_tile", _i), ("workspace", _vp), ("workspace_bytes", _sz), ("unsorted", _i),
                 ("kc_mx_scale", _vp), ("device_status", _vp)]
+
+
+class _Cache(ctypes.Structure):
+    """si_cache."""
+    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("k_scale", _vp), ("v_scale", _vp), ("n_pages", _i),
+                ("H_kv", _i), ("page", _i), ("D", _i)]
 
 
 _ARGS = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]
@@ -68,6 +74,25 @@ _lib.si_two_stage_workspace_size.argtypes = [_i] * 6
 _lib.si_sparse_attention.restype = _i
 _lib.si_sparse_attention.argtypes = [_vp, _vp, _vp] + [_i] * 7 + [ctypes.c_float, _vp, _vp, _vp,
                                                                     ctypes.POINTER(Options)]
+_cp = ctypes.POINTER(_Cache)
+_lib.si_cache_append.restype = _i
+_lib.si_cache_append.argtypes = [_cp] + [_vp] * 5 + [_i] * 4 + [_vp]
+_lib.si_cache_attention.restype = _i
+_lib.si_cache_attention.argtypes = ([_vp, _cp, _vp, _vp] + [_i] * 6 + [ctypes.c_float, _i, _vp, _vp, _vp,
+                                                                       ctypes.POINTER(Options)])
+_lib.si_cache_attention_workspace_size.restype = _sz
+_lib.si_cache_attention_workspace_size.argtypes = [_i]
+_lib.si_window_attention.restype = _i
+_lib.si_window_attention.argtypes = [_vp] * 4 + [_i] * 7 + [ctypes.c_float, _i, _vp, _vp, _vp,
+                                                            ctypes.POINTER(Options)]
+_lib.si_cache_reserve.restype = _i
+_lib.si_cache_reserve.argtypes = [_cp] + [_vp] * 4 + [_i] * 2 + [_vp] * 2
+_lib.si_cache_fork.restype = _i
+_lib.si_cache_fork.argtypes = [_cp] + [_vp] * 5 + [_i] * 4 + [_vp] * 2
+_lib.si_cache_free.restype = _i
+_lib.si_cache_free.argtypes = [_vp] * 4 + [_i] * 4 + [_vp]
+_lib.si_cache_compact.restype = _i
+_lib.si_cache_compact.argtypes = [_cp] + [_vp] * 2 + [_i] * 2 + [_vp] * 3
 _lib.si_mxfp4_to_bf16.restype = _i
 _lib.si_mxfp4_to_bf16.argtypes = [_vp, _vp, ctypes.c_int64, _i, _vp, _vp]
 _lib.si_device_status.restype = _i
@@ -261,6 +286,241 @@ def sparse_attention(q, kv, idx, *, scale: float = 0.0, out=None, lse=None, stre
                                     float(scale), out.data_ptr(), lse.data_ptr(), _stream_ptr(stream),
                                     ctypes.byref(o)), "si_sparse_attention")
     return out, lse
+
+
+_FLOAT_DTYPES = {torch.bfloat16: SI_DTYPE_BF16, torch.float16: SI_DTYPE_FP16}
+
+
+def _need(name, t, dtype, device, shape=None):
+    """A contiguous CUDA tensor of the dtype, on the device (and of the shape)."""
+    if t.dtype != dtype or t.device != device or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device if device.type == 'cuda' else 'CUDA'}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have the shape {shape} (got {tuple(t.shape)})")
+
+
+def _float_dtype(name, t):
+    dt = _FLOAT_DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be bfloat16 or float16 (got {t.dtype})")
+    return dt
+
+
+def _enqueue(where, device, stream, call):
+    """call(stream pointer) on `stream`, or on the current stream of `device`,
+    with that device current for the launches."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if torch.cuda.current_device() == device.index:
+        st = call(stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = call(stream.cuda_stream)
+    if st != SI_OK:
+        raise SIError(st, where)
+
+
+class PagedCache:
+    """A paged K/V cache (``si_cache``): k_pages and v_pages [n_pages, H_kv,
+    page, D] e4m3 codes (float8_e4m3fn or uint8), k_scale and v_scale
+    [n_pages, H_kv] fp32; value = code * scale.  page is 16, 32, 64 or 128, D
+    64 or 128.  Holds the tensors; the state of the sequences (page table,
+    lengths, reference counts) stays with the caller."""
+
+    def __init__(self, k_pages, v_pages, k_scale, v_scale):
+        if k_pages.dim() != 4 or k_pages.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise ValueError("k_pages [n_pages, H_kv, page, D] must hold e4m3 codes (float8_e4m3fn or uint8)")
+        device = k_pages.device
+        _need("k_pages", k_pages, k_pages.dtype, device)
+        _need("v_pages", v_pages, k_pages.dtype, device, tuple(k_pages.shape))
+        _need("k_scale", k_scale, torch.float32, device, tuple(k_pages.shape[:2]))
+        _need("v_scale", v_scale, torch.float32, device, tuple(k_pages.shape[:2]))
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
+        self.device = device
+        self.n_pages, self.kv_heads, self.page, self.dim = k_pages.shape
+        self._c = _Cache(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                         self.n_pages, self.kv_heads, self.page, self.dim)
+
+
+def cache_append(cache: PagedCache, k, v, table, lens, *, n_new=None, stream=None):
+    """Appends rows to the sequences of a cache (``si_cache_append``): k, v
+    [B, L, H_kv, D] bf16 or fp16, table [B, max_pages] int32, lens [B] int32
+    (tokens held before; not changed), n_new [B] int32 (default: L each).  The
+    pages must be there (cache_reserve)."""
+    if k.dim() != 4 or table.dim() != 2:
+        raise ValueError("k, v [B, L, H_kv, D] and table [B, max_pages] expected")
+    B, L = k.shape[:2]
+    dt = _float_dtype("k", k)
+    device = cache.device
+    shape = (B, L, cache.kv_heads, cache.dim)
+    _need("k", k, k.dtype, device, shape)
+    _need("v", v, k.dtype, device, shape)
+    _need("table", table, torch.int32, device, (B, table.shape[1]))
+    _need("lens", lens, torch.int32, device, (B,))
+    if n_new is not None:
+        _need("n_new", n_new, torch.int32, device, (B,))
+    _enqueue("si_cache_append", device, stream, lambda s: _lib.si_cache_append(
+        cache._c, k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(),
+        n_new.data_ptr() if n_new is not None else None, B, L, table.shape[1], dt, s))
+
+
+def _attention_outputs(q, out, lse):
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need("out", out, q.dtype, q.device, tuple(q.shape))
+    if lse is None:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    else:
+        _need("lse", lse, torch.float32, q.device, tuple(q.shape[:3]))
+    return out, lse
+
+
+def _attention_options(device, workspace, device_status):
+    if workspace is None and device_status is None:
+        return None
+    o = Options()
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        o.workspace = workspace.data_ptr()
+        o.workspace_bytes = workspace.numel() * workspace.element_size()
+    if device_status is not None:
+        if device_status.numel() < 2:
+            raise ValueError("device_status must hold at least 2 elements")
+        _need("device_status", device_status, torch.int32, device)
+        o.device_status = device_status.data_ptr()
+    return o
+
+
+def cache_attention(q, cache: PagedCache, table, lens, *, window: int = 0, n_sink: int = 0, scale: float = 0.0,
+                    out=None, lse=None, workspace=None, stream=None, device_status=None):
+    """Attention of each sequence's last L tokens over its cache
+    (``si_cache_attention``): q [B, L, H, D] bf16 or fp16, table [B,
+    max_pages] int32, lens [B] int32 (tokens in the cache, the queries' own
+    among them).  window 0 sees everything before; else the last `window`
+    tokens and the first `n_sink`.  Returns (out [B, L, H, D], lse [B, L, H]
+    fp32).  workspace: optional scratch of
+    cache_attention_workspace_size() bytes."""
+    if q.dim() != 4 or table.dim() != 2:
+        raise ValueError("q [B, L, H, D] and table [B, max_pages] expected")
+    B, L, H, D = q.shape
+    dt = _float_dtype("q", q)
+    device = cache.device
+    if D != cache.dim:
+        raise ValueError(f"q has {D} dims a head, the cache {cache.dim}")
+    _need("q", q, q.dtype, device)
+    _need("table", table, torch.int32, device, (B, table.shape[1]))
+    _need("lens", lens, torch.int32, device, (B,))
+    out, lse = _attention_outputs(q, out, lse)
+    o = _attention_options(device, workspace, device_status)
+    _enqueue("si_cache_attention", device, stream, lambda s: _lib.si_cache_attention(
+        q.data_ptr(), cache._c, table.data_ptr(), lens.data_ptr(), B, L, H, table.shape[1], window, n_sink, scale,
+        dt, out.data_ptr(), lse.data_ptr(), s, o))
+    return out, lse
+
+
+def cache_attention_workspace_size(D: int) -> int:
+    """Scratch bytes that suffice for any cache_attention call with D on the current device."""
+    return int(_lib.si_cache_attention_workspace_size(D))
+
+
+def window_attention(q, k, v, *, window: int, n_sink: int = 0, lens=None, scale: float = 0.0, out=None, lse=None,
+                     stream=None, device_status=None):
+    """Attention of whole prompts through a sliding window with sinks
+    (``si_window_attention``): q [B, S, H, D], k and v [B, S, H_kv, D], bf16 or
+    fp16; lens [B] int32 (default: S each), the rest is padding.  Returns
+    (out [B, S, H, D], lse [B, S, H] fp32); padded rows give 0 and -inf."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q [B, S, H, D] and k, v [B, S, H_kv, D] expected")
+    B, S, H, D = q.shape
+    dt = _float_dtype("q", q)
+    device = q.device
+    _need("q", q, q.dtype, device)
+    shape = (B, S, k.shape[2], D)
+    _need("k", k, q.dtype, device, shape)
+    _need("v", v, q.dtype, device, shape)
+    if lens is not None:
+        _need("lens", lens, torch.int32, device, (B,))
+    out, lse = _attention_outputs(q, out, lse)
+    o = _attention_options(device, None, device_status)
+    _enqueue("si_window_attention", device, stream, lambda s: _lib.si_window_attention(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr() if lens is not None else None, B, S, H,
+        k.shape[2], D, window, n_sink, scale, dt, out.data_ptr(), lse.data_ptr(), s, o))
+    return out, lse
+
+
+def _sequence_state(cache, table, lens, refs):
+    if table.dim() != 2:
+        raise ValueError("table [n_seq, max_pages] expected")
+    _need("table", table, torch.int32, cache.device)
+    if lens is not None:
+        _need("lens", lens, torch.int32, cache.device, (table.shape[0],))
+    _need("refs", refs, torch.int32, cache.device, (cache.n_pages,))
+    return table.shape
+
+
+def cache_reserve(cache: PagedCache, table, lens, refs, n_new, *, status=None, stream=None):
+    """Gives every sequence the pages for n_new[b] more tokens
+    (``si_cache_reserve``): table [n_seq, max_pages], lens [n_seq], refs
+    [n_pages], n_new [n_seq] int32; table and refs are updated.  Returns
+    status [n_seq] int32: 0 done, 1 too few free pages, 2 more than max_pages."""
+    n_seq, max_pages = _sequence_state(cache, table, lens, refs)
+    _need("n_new", n_new, torch.int32, cache.device, (n_seq,))
+    if status is None:
+        status = torch.empty((n_seq,), dtype=torch.int32, device=cache.device)
+    else:
+        _need("status", status, torch.int32, cache.device, (n_seq,))
+    _enqueue("si_cache_reserve", cache.device, stream, lambda s: _lib.si_cache_reserve(
+        cache._c, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), n_new.data_ptr(), n_seq, max_pages,
+        status.data_ptr(), s))
+    return status
+
+
+def cache_fork(cache: PagedCache, table, lens, refs, src, dst, *, share: bool = True, status=None, stream=None):
+    """Makes row dst[i] a copy of row src[i] (``si_cache_fork``), sharing the
+    full pages (share) or copying all of them; table, lens and refs are
+    updated.  Returns status [n] int32: 0 done, 1 too few free pages, 2 not
+    possible (an index out of range, dst not empty or named twice)."""
+    n_seq, max_pages = _sequence_state(cache, table, lens, refs)
+    n = src.numel()
+    _need("src", src, torch.int32, cache.device, (n,))
+    _need("dst", dst, torch.int32, cache.device, (n,))
+    if status is None:
+        status = torch.empty((n,), dtype=torch.int32, device=cache.device)
+    else:
+        _need("status", status, torch.int32, cache.device, (n,))
+    _enqueue("si_cache_fork", cache.device, stream, lambda s: _lib.si_cache_fork(
+        cache._c, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), src.data_ptr(), dst.data_ptr(), n, n_seq,
+        max_pages, int(bool(share)), status.data_ptr(), s))
+    return status
+
+
+def cache_free(cache: PagedCache, table, lens, refs, rows, *, stream=None):
+    """Frees the sequences of the given rows (``si_cache_free``): table, lens and refs are updated."""
+    n_seq, max_pages = _sequence_state(cache, table, lens, refs)
+    n = rows.numel()
+    _need("rows", rows, torch.int32, cache.device, (n,))
+    _enqueue("si_cache_free", cache.device, stream, lambda s: _lib.si_cache_free(
+        table.data_ptr(), lens.data_ptr(), refs.data_ptr(), rows.data_ptr(), n, n_seq, max_pages, cache.n_pages, s))
+
+
+def cache_compact(cache: PagedCache, table, refs, *, used=None, moved=None, stream=None):
+    """Moves the pages in use together (``si_cache_compact``); table and refs
+    are updated.  Returns (used [1] int32, the number of pages in use; moved
+    [n_pages] int32, each used page's new place, -1 for the others)."""
+    n_seq, max_pages = _sequence_state(cache, table, None, refs)
+    if used is None:
+        used = torch.empty((1,), dtype=torch.int32, device=cache.device)
+    else:
+        _need("used", used, torch.int32, cache.device, (1,))
+    if moved is None:
+        moved = torch.empty((cache.n_pages,), dtype=torch.int32, device=cache.device)
+    else:
+        _need("moved", moved, torch.int32, cache.device, (cache.n_pages,))
+    _enqueue("si_cache_compact", cache.device, stream, lambda s: _lib.si_cache_compact(
+        cache._c, table.data_ptr(), refs.data_ptr(), n_seq, max_pages, used.data_ptr(), moved.data_ptr(), s))
+    return used, moved
 
 
 def mxfp4_to_bf16(codes, scales, out=None, stream=None):

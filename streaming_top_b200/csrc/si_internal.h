@@ -86,6 +86,9 @@ si_status launch_sparse_attention(const void* q, const void* kv, const int32_t* 
                                   float scale, void* out, float* lse, int* err, uint64_t wait_limit_ns,
                                   cudaStream_t stream);
 
+// Checks the description of a paged K/V cache.
+si_status check_cache(const si_cache* c);
+
 // Decodes MXFP4 rows (codes [rows, D/2], E8M0 scales [rows, D/32]) to bf16 [rows, D].
 si_status launch_mxfp4_to_bf16(const void* codes, const void* scales, long long rows, int D, void* out,
                                cudaStream_t stream);
