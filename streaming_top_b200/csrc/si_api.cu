@@ -64,8 +64,6 @@ EncodeTiledFn g_encode = nullptr;
 std::once_flag g_encode_once;
 cudaError_t g_encode_err = cudaSuccess;
 
-constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;  // 2 s per bounded wait
-
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace
@@ -126,9 +124,8 @@ si_status scratch_alloc(void** p, size_t bytes, cudaStream_t stream, const char*
   return fail(SI_ERR_OUT_OF_MEMORY, "cudaMallocFromPoolAsync(%zu) for %s: %s", bytes, what, cudaGetErrorString(e));
 }
 
-si_status encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
-                         uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
-                         uint32_t box_outer) {
+si_status encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base, const uint64_t* dims,
+                      const uint64_t* stride_bytes, const uint32_t* box, int swizzle) {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -137,15 +134,28 @@ si_status encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void
       g_encode = reinterpret_cast<EncodeTiledFn>(fn);
   });
   if (!g_encode) return fail(SI_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (%s)", cudaGetErrorString(g_encode_err));
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = g_encode(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5];
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    if (i) st[i - 1] = stride_bytes[i - 1];
+  }
+  const CUresult r = g_encode(map, dtype, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, bx, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SI_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
   return SI_OK;
+}
+
+si_status encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
+                         uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
+                         uint32_t box_outer) {
+  const uint64_t dims[2] = {inner, outer};
+  const uint32_t box[2] = {box_inner, box_outer};
+  return encode_tmap(map, dtype, 2, base, dims, &row_bytes, box, 128);
 }
 
 bool try_encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t dims[3],

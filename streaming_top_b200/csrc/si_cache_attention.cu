@@ -1,120 +1,963 @@
-// Attention over the paged 8-bit K/V cache, and of prompts through the window.
+// Attention over the paged 8-bit K/V cache: the last L tokens of each
+// sequence against everything they see of it.
 //
-// One warp per (sequence, query, head): it walks the visible keys with the
-// running maximum and sum of the softmax, every lane holding D / 32 dims.
+// What bounds it: every visible token costs 2 D bytes of HBM a key/value head
+// and 4 D flops a query row.  With up to some 64 rows a head the bytes decide,
+// so the kernel is built to read each page once, at full rate, and never to
+// touch a code with an ALU:
+//   S^T[token, row] = K[token, :] . q[row, :]     A = 128 cached tokens (e4m3, as TMA brings them), B = q
+//   O^T[dim, row]   = sum_token V[token, dim] P   A = V read along dims (MN-major), B = P
+// Both are tcgen05 kind::f8f6f4 products with the tokens (or dims) on the 128
+// lanes and the few query rows on N, so no lane of the tensor core's M is
+// padding.  q and the softmax weights, which have more bits than e4m3, enter
+// as sums of e4m3 terms (two carry 8 bits, bf16's own precision; three the 11
+// of fp16): q = 2^x (t0 + t1 [+ t2]), each term the rounded rest, accumulated
+// into the same fp32 accumulator by one more pass of the same MMA.  With x
+// from the row's largest magnitude (224 .. 448) bf16's terms are exact down to
+// 2^-14 of it, then off by 2^-19 of it at most.  P is scaled likewise: a
+// tile's weights are taken relative to the tile's own maximum and to its
+// largest value scale, P = 256 exp2(s - m_tile) v_scale / v_ref, so that a tile
+// far below the running maximum keeps its precision, and the value scales cost
+// nothing.  The running state joins tiles as usual, in fp32.
+//
+// Work: tiles of 128 tokens.  All CTAs get equal runs of consecutive tiles of
+// the whole batch (sequence, head, rows, tile), whatever its lengths; a unit
+// (sequence, head, row chunk) that a run's border cuts leaves partial results
+// (maximum, sum, unnormalised O) in one of its CTA's two slots, which a second
+// kernel joins.  Where a unit has few tiles at most, units are not cut and no
+// second kernel is launched.
+//
+// Warps: 0 schedules (walks the tiles, reads page table and scales ahead,
+// publishes tile descriptors) and loads pages by TMA; 1 issues the MMAs; 2-3
+// split the queries into terms; 4-11 do the softmax: the two warpgroups take
+// half of the rows each, a thread one token (and later one dim).
+// Every wait is bounded; on expiry SI_ERR_TIMEOUT is recorded, copies and MMAs
+// in flight are drained and the kernel exits.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
 #include "si_internal.h"
+#include "si_ptx.cuh"
 
 namespace si {
 namespace {
 
-struct RowParams {
-  const uint8_t *q, *k, *v;
+constexpr int C_THREADS = 384;
+constexpr int C_TILE = 128;      // tokens of a tile
+constexpr int C_ND = 8;          // tile descriptors in flight
+constexpr int C_WHOLE = 4;       // units of at most this many tiles are not cut
+constexpr int C_MAX_CTAS = 512;  // of a launch
+constexpr int C_MIN_RUN = 2;     // tiles a CTA gets at least when units are cut
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+enum { CERR_SLOT = 41, CERR_DESC = 42, CERR_FULL = 43, CERR_Q = 44, CERR_S = 45, CERR_P = 46, CERR_O = 47,
+       CERR_X = 48, CERR_DRAIN = 49 };
+
+enum { F_FIRST = 1, F_LAST = 2, F_MASK = 4 };  // of the CTA's segment of a unit; not every row sees every token
+
+struct CacheParams {
+  const uint8_t* q;
   const float *ks, *vs;
   const int32_t *table, *lens;
   uint8_t* out;
   float* lse;
-  int B, L, H, H_kv, page, max_pages, n_pages, window, n_sink;
-  float scale;
+  float* part;       // partial results: [2 * CTAs] slots of rows x (D + 2) floats
+  int4* meta;        // [CTAs]: the unit that begins in the CTA and goes on, the CTAs it spans, its slot
+  int* err;
+  long long rows_total;  // rows of the pools
+  int B, L, H, H_kv, G, page, max_pages, n_pages, window, n_sink, chunks, cut;
+  float scale_log2;
+  uint64_t wait_limit_ns;
 };
 
-template <bool HALF>
-__device__ __forceinline__ float load16(const uint8_t* p, size_t i) {
-  if (HALF) return __half2float(reinterpret_cast<const __half*>(p)[i]);
-  return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
+// A tile, as the scheduler publishes it.
+struct TileDesc {
+  int flags, tok0, b, h, row0, rows, vslot, vparity;
+  int p_lo, p_hi;       // positions of the sequence's first and last query
+  int pages;            // bit j: page j of the tile is there
+  int seg;              // 0: the CTA's first segment of a unit, 1: a later one (its slot)
+  int left;             // the unit's tiles behind this one
+  float vref;
+  float ks[8], rv[8];   // a page's key scale, and value scale / v_ref * 256
+};
+
+// The visible tiles of a sequence: n_sink_tiles from 0 on, then those from `first` on.
+struct Span {
+  int first, sink_tiles, tiles;
+  long long lo, hi, sink;  // visible tokens: [0, sink) and [lo, hi)
+  int p_lo, p_hi;
+};
+
+__device__ __forceinline__ Span span_of(const CacheParams& p, int b) {
+  Span s;
+  const long long len = p.lens[b], cap = static_cast<long long>(p.max_pages) * p.page;
+  const long long p_lo = len - p.L, p_hi = len - 1;
+  s.hi = max(min(p_hi + 1, cap), 0ll);
+  s.lo = p.window ? min(max(p_lo - p.window + 1, 0ll), s.hi) : 0;
+  s.sink = p.window ? min(static_cast<long long>(p.n_sink), s.hi) : 0;
+  s.first = static_cast<int>(s.lo / C_TILE);
+  const int main_tiles = static_cast<int>((s.hi + C_TILE - 1) / C_TILE) - s.first;
+  s.sink_tiles = min(static_cast<int>((s.sink + C_TILE - 1) / C_TILE), s.first);
+  s.tiles = max(main_tiles + s.sink_tiles, 1);  // an empty unit still writes its rows
+  s.p_lo = static_cast<int>(max(p_lo, -(1ll << 30)));
+  s.p_hi = static_cast<int>(p_hi < 0 ? -1 : p_hi);
+  return s;
 }
 
-__device__ __forceinline__ float load8(const uint8_t* p, size_t i) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(p[i], __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half*>(&h));
+__device__ __forceinline__ void cache_error(const CacheParams& p, volatile int* abort, int where) {
+  atomicCAS(p.err, 0, static_cast<int>(SI_ERR_TIMEOUT));
+  atomicCAS(p.err + 1, 0, where);
+  *abort = 1;
 }
 
-template <int D, bool HALF, bool PAGED>
-__global__ void __launch_bounds__(128) row_attention_kernel(const RowParams p) {
-  constexpr int N = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(p.B) * p.L * p.H) return;
-  const int h = static_cast<int>(row % p.H);
-  const int i = static_cast<int>(row / p.H % p.L), b = static_cast<int>(row / p.H / p.L);
-  const int g = h / (p.H / p.H_kv);
-  long long len = p.lens ? p.lens[b] : p.L;
-  long long pos;
-  if (PAGED) {
-    pos = len - p.L + i;
-    len = min(len, static_cast<long long>(p.max_pages) * p.page);
-  } else {
-    len = min(max(len, 0ll), static_cast<long long>(p.L));
-    pos = i < len ? i : -1;
-  }
-  float q[N], acc[N], m = -INFINITY, sum = 0.f;
-  for (int d = 0; d < N; ++d) {
-    q[d] = load16<HALF>(p.q, static_cast<size_t>(row) * D + d * 32 + lane);
-    acc[d] = 0.f;
-  }
-  const long long stop = min(pos + 1, len);
-  long long first = p.window ? max(pos - p.window + 1, 0ll) : 0;
-  for (long long j = p.window ? 0 : first; j < stop; ++j) {
-    if (j >= p.n_sink && j < first) j = first;
-    if (j >= stop) break;
-    float kv[N], vv[N];
-    if (PAGED) {
-      const int id = p.table[static_cast<size_t>(b) * p.max_pages + j / p.page];
-      if (id < 0 || id >= p.n_pages) continue;
-      const size_t ph = static_cast<size_t>(id) * p.H_kv + g, at = (ph * p.page + j % p.page) * D;
-      for (int d = 0; d < N; ++d) {
-        kv[d] = load8(p.k, at + d * 32 + lane) * p.ks[ph];
-        vv[d] = load8(p.v, at + d * 32 + lane) * p.vs[ph];
-      }
-    } else {
-      const size_t at = ((static_cast<size_t>(b) * p.L + j) * p.H_kv + g) * D;
-      for (int d = 0; d < N; ++d) {
-        kv[d] = load16<HALF>(p.k, at + d * 32 + lane);
-        vv[d] = load16<HALF>(p.v, at + d * 32 + lane);
-      }
-    }
-    float s = 0.f;
-    for (int d = 0; d < N; ++d) s += q[d] * kv[d];
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    s *= p.scale;
-    const float mn = fmaxf(m, s), c = m == mn ? 1.f : __expf(m - mn), e = s == mn ? 1.f : __expf(s - mn);
-    m = mn;
-    sum = sum * c + e;
-    for (int d = 0; d < N; ++d) acc[d] = acc[d] * c + e * vv[d];
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  for (int d = 0; d < N; ++d) {
-    const size_t at = static_cast<size_t>(row) * D + d * 32 + lane;
-    if (HALF) reinterpret_cast<__half*>(p.out)[at] = __float2half_rn(acc[d] * inv);
-    else reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(acc[d] * inv);
-  }
-  if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? m + logf(sum) : -INFINITY;
+// Matrix descriptors: `type` 2 = 128-byte swizzle, 4 = 64-byte, 0 = none.
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t type) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+         static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32 | static_cast<uint64_t>(1u) << 46 |
+         static_cast<uint64_t>(type) << 61;
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-template <bool PAGED>
-si_status launch_rows(const RowParams& p, int D, int dtype, cudaStream_t s) {
-  const long long rows = static_cast<long long>(p.B) * p.L * p.H;
-  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-  const bool half = dtype == SI_DTYPE_FP16;
-  if (D == 128) {
-    if (half) row_attention_kernel<128, true, PAGED><<<grid, 128, 0, s>>>(p);
-    else row_attention_kernel<128, false, PAGED><<<grid, 128, 0, s>>>(p);
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                 : "r"(addr));
+  } else if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "r"(addr));
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(addr));
   } else {
-    if (half) row_attention_kernel<64, true, PAGED><<<grid, 128, 0, s>>>(p);
-    else row_attention_kernel<64, false, PAGED><<<grid, 128, 0, s>>>(p);
+    static_assert(N == 32, "columns");
+    tmem_ld32(addr, *reinterpret_cast<uint32_t(*)[32]>(v));
   }
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? SI_OK : cuda_fail(e, "row_attention_kernel launch");
 }
+
+// The largest of a value over the warp (NaN loses).
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// v[0..3] -= the values of four codes.
+__device__ __forceinline__ void take_off(float (&v)[4], uint32_t codes) {
+  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xFFFFu), __NV_E4M3);
+  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes >> 16), __NV_E4M3);
+  const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  v[0] -= fa.x;
+  v[1] -= fa.y;
+  v[2] -= fb.x;
+  v[3] -= fb.y;
+}
+
+// Sizes of an instantiation: R query rows of a unit (8, 16, 32 or 64).
+template <int D, int R, bool HALF>
+struct CacheShape {
+  static constexpr int N = R < 16 ? 16 : R;    // the MMAs' N
+  static constexpr int TERMS = HALF ? 3 : 2;   // e4m3 terms of q and of P
+  static constexpr int CTAS = R <= 16 ? 2 : 1; // per SM
+  static constexpr int SLOT = C_TILE * D;      // a K or V tile
+  static constexpr int Q = TERMS * N * D;      // one q buffer
+  static constexpr int P = TERMS * N * C_TILE; // one P buffer
+  static constexpr int SLOTS = CTAS == 2 ? (D == 128 ? 5 : 10) : (R == 32 || D == 64 ? 8 : 6);
+  static constexpr int TMEM = 4 * N;           // S and O, two buffers each
+};
+
+template <int D, int R, bool HALF>
+struct CacheCtrl {
+  using Sh = CacheShape<D, R, HALF>;
+  uint64_t full[Sh::SLOTS], empty[Sh::SLOTS];
+  uint64_t d_full[C_ND], d_empty[C_ND];
+  uint64_t q_full[2], q_empty[2], s_full[2], s_empty[2], p_full[2], o_full[2], o_empty[2], xbar, done;
+  TileDesc desc[C_ND];
+  alignas(16) float qs[2][R];         // score scale of a row
+  alignas(16) int pos[2][R];          // a row's position; -1: sees nothing
+  alignas(16) int low[2][R];          // tokens at or below are before its window
+  alignas(16) float red[2][R][4];     // per row and quadrant of lanes: the tile's maximum
+  alignas(16) float sum[R][4];        // the same: the unit's sum
+  alignas(16) float2 ab[2][R];        // per row: factors of the state and of the tile's O
+  uint32_t nan_bits[2][C_TILE][4];    // dims whose value is NaN, for tokens that only some rows see
+  int nan_tile[2];
+  long long scan[C_THREADS / 32];
+  long long total, start, stop;       // tiles of the batch; this CTA's run
+  int b0;                             // the sequence in which the run starts,
+  long long before0;                  // and the tiles of one (head, chunk) in the sequences before it
+  uint32_t tmem_slot;
+  int abort;
+};
+
+template <int D, int R, bool HALF>
+__global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
+    cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                           const CacheParams p) {
+  using Sh = CacheShape<D, R, HALF>;
+  constexpr int N = Sh::N, TERMS = Sh::TERMS, NS = Sh::SLOTS, HC = R / 2;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* kv_s = smem;
+  uint8_t* q_s = kv_s + NS * Sh::SLOT;
+  uint8_t* p_s = q_s + 2 * Sh::Q;
+  auto* C = reinterpret_cast<CacheCtrl<D, R, HALF>*>(p_s + 2 * Sh::P);
+  volatile int* abort = &C->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t limit = p.wait_limit_ns;
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&C->full[s], 1);
+      mbar_init(&C->empty[s], 1);
+    }
+    for (int s = 0; s < C_ND; ++s) {
+      mbar_init(&C->d_full[s], 1);
+      mbar_init(&C->d_empty[s], 11);  // MMA, two q warps, eight softmax warps
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&C->q_full[s], 2);
+      mbar_init(&C->q_empty[s], 9);   // the MMAs' commit, eight softmax warps
+      mbar_init(&C->s_full[s], 1);
+      mbar_init(&C->s_empty[s], 8);
+      mbar_init(&C->p_full[s], 8);
+      mbar_init(&C->o_full[s], 1);
+      mbar_init(&C->o_empty[s], 8);
+      C->nan_tile[s] = -1;
+    }
+    mbar_init(&C->xbar, 8);
+    mbar_init(&C->done, 1);
+    *abort = 0;
+    if (p.cut) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    fence_mbar_init();
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == 1) tmem_alloc(&C->tmem_slot, Sh::TMEM);
+
+  // ---- this CTA's run of tiles
+  const int HN = p.H_kv * p.chunks;
+  if (p.cut) {
+    long long sum = 0;
+    for (int b = tid; b < p.B; b += C_THREADS) sum += span_of(p, b).tiles;
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) C->scan[warp] = sum;
+    __syncthreads();
+    if (tid == 0) {
+      long long t = 0;
+      for (int w = 0; w < C_THREADS / 32; ++w) t += C->scan[w];
+      t *= HN;
+      // fewer CTAs than the grid where their runs would get too short
+      const long long n = min(static_cast<long long>(gridDim.x), max(t / C_MIN_RUN, 1ll));
+      C->total = t;
+      C->start = blockIdx.x < n ? blockIdx.x * t / n : t;
+      C->stop = blockIdx.x < n ? (blockIdx.x + 1) * t / n : t;
+    }
+    __syncthreads();
+    // the sequence in which the run starts
+    long long run = 0;
+    const long long start = C->start;
+    for (int base = 0; base < p.B && start < C->total; base += C_THREADS) {
+      const int b = base + tid;
+      const long long t = b < p.B ? span_of(p, b).tiles : 0;
+      long long inc = t;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      if (lane == 31) C->scan[warp] = inc;
+      __syncthreads();
+      long long before = run, all = run;
+      for (int w = 0; w < C_THREADS / 32; ++w) {
+        if (w < warp) before += C->scan[w];
+        all += C->scan[w];
+      }
+      before += inc - t;
+      if (t > 0 && before * HN <= start && start < (before + t) * HN) {
+        C->b0 = b;
+        C->before0 = before;
+      }
+      run = all;
+      __syncthreads();
+      if (all * HN > start) break;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = C->tmem_slot;
+
+  // n_tiles of this CTA, the first at tile k0 of unit (b0, hn0)
+  const int n_cta = p.cut ? static_cast<int>(min(static_cast<long long>(gridDim.x), max(C->total / C_MIN_RUN, 1ll)))
+                          : static_cast<int>(gridDim.x);
+  long long n_tiles = 0;
+  int b0 = 0, hn0 = 0, k0 = 0;
+  long long u_stop = 0;  // whole units: the run's end
+  if (p.cut) {
+    n_tiles = C->stop - C->start;
+    if (n_tiles > 0) {
+      b0 = C->b0;
+      const int t = span_of(p, b0).tiles;
+      const long long in_b = C->start - C->before0 * HN;
+      hn0 = static_cast<int>(in_b / t);
+      k0 = static_cast<int>(in_b % t);
+    }
+  } else {
+    const long long U = static_cast<long long>(p.B) * HN;
+    const long long u0 = U * blockIdx.x / n_cta;
+    u_stop = U * (blockIdx.x + 1) / n_cta;
+    if (u0 < u_stop) {
+      b0 = static_cast<int>(u0 / HN);
+      hn0 = static_cast<int>(u0 % HN);
+      for (long long u = u0; u < u_stop;) {
+        const int b = static_cast<int>(u / HN);
+        const long long e = min(u_stop, (b + 1ll) * HN);
+        n_tiles += (e - u) * span_of(p, b).tiles;
+        u = e;
+      }
+    }
+  }
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ scheduler and TMA
+    const int npg = C_TILE / p.page, group = 32 / npg;  // pages of a tile; tiles that the warp looks up at once
+    const int gi = lane / npg, pj = lane % npg;
+    int b = b0, hn = hn0, k = k0;
+    Span sp = n_tiles ? span_of(p, b) : Span{};
+    uint32_t slot = 0, phase = 0, any = 0, last_par = 0;
+    long long t = 0;
+    int seg = 0;
+    bool stop = false;
+    while (t < n_tiles && !stop) {
+      // up to `group` tiles of this unit: lane (gi, pj) looks up page pj of tile k + gi
+      const int h = hn / p.chunks, row0 = (hn % p.chunks) * R;
+      const int cnt = static_cast<int>(min(static_cast<long long>(min(group, sp.tiles - k)), n_tiles - t));
+      const int kk = k + gi;
+      const int tile = kk < sp.sink_tiles ? kk : sp.first + kk - sp.sink_tiles;
+      const long long tok = static_cast<long long>(tile) * C_TILE + pj * p.page;
+      bool there = gi < cnt && tok < sp.hi && (tok + p.page > sp.lo || tok < sp.sink);
+      int id = -1;
+      if (there) id = p.table[static_cast<size_t>(b) * p.max_pages + tok / p.page];
+      there = there && id >= 0 && id < p.n_pages;
+      const size_t ph = static_cast<size_t>(there ? id : 0) * p.H_kv + h;
+      const float ks = there ? p.ks[ph] : 0.f, vs = there ? p.vs[ph] : 0.f;
+      // coordinates past the pool read zeros
+      const int y = there ? static_cast<int>(ph * p.page) : static_cast<int>(p.rows_total);
+      const uint32_t there_bits = __ballot_sync(0xFFFFFFFFu, there);
+      float vref = vs;
+      for (int o = npg >> 1; o; o >>= 1) vref = fmaxf(vref, __shfl_xor_sync(0xFFFFFFFFu, vref, o));
+      const float rv = vref > 0.f ? vs / vref * 256.f : 0.f;
+      for (int i = 0; i < cnt; ++i, ++t) {
+        const int ds = static_cast<int>(t % C_ND);
+        if (!mbar_wait_bounded(&C->d_empty[ds], (static_cast<uint32_t>(t / C_ND) & 1u) ^ 1u, abort, limit)) {
+          if (lane == 0) cache_error(p, abort, CERR_DESC);
+          stop = true;
+          break;
+        }
+        TileDesc& d = C->desc[ds];
+        uint32_t vslot = slot + 1, vphase = phase;
+        if (vslot == NS) {
+          vslot = 0;
+          vphase ^= 1u;
+        }
+        if (gi == i) {
+          d.ks[pj] = ks;
+          d.rv[pj] = rv;
+          if (pj == 0) {
+            const long long tok0 = static_cast<long long>(tile) * C_TILE;
+            const uint32_t pages = (there_bits >> (gi * npg)) & (npg == 32 ? ~0u : (1u << npg) - 1u);
+            const bool all = pages == (1u << npg) - 1u && tok0 + C_TILE - 1 <= sp.p_lo &&
+                             (!p.window || tok0 > static_cast<long long>(sp.p_hi) - p.window || tok0 + C_TILE <= p.n_sink);
+            const bool first = t == 0 || kk == 0, last = t == n_tiles - 1 || kk == sp.tiles - 1;
+            d.flags = (first ? F_FIRST : 0) | (last ? F_LAST : 0) | (all ? 0 : F_MASK);
+            d.tok0 = static_cast<int>(tok0);
+            d.b = b;
+            d.h = h;
+            d.row0 = row0;
+            d.rows = min(R, p.L * p.G - row0);
+            d.vslot = static_cast<int>(vslot);
+            d.vparity = static_cast<int>(vphase);
+            d.p_lo = sp.p_lo;
+            d.p_hi = sp.p_hi;
+            d.pages = static_cast<int>(pages);
+            d.seg = seg;
+            d.left = sp.tiles - 1 - kk;
+            d.vref = vref;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C->d_full[ds]);
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!mbar_wait_bounded(&C->empty[slot], phase ^ 1u, abort, limit)) {
+            if (lane == 0) cache_error(p, abort, CERR_SLOT);
+            stop = true;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&C->full[slot], Sh::SLOT);
+          __syncwarp();
+          if (gi == i) tma_load_2d(kv_s + slot * Sh::SLOT + pj * p.page * D, kv ? &tm_v : &tm_k, &C->full[slot], 0, y);
+          any |= 1u << slot;
+          last_par = (last_par & ~(1u << slot)) | (phase << slot);
+          if (++slot == NS) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+        if (stop) break;
+      }
+      k += cnt;
+      if (k == sp.tiles) {
+        k = 0;
+        seg = 1;
+        if (++hn == HN) {
+          hn = 0;
+          ++b;
+          if (b < p.B && t < n_tiles) sp = span_of(p, b);
+        }
+      }
+    }
+    __syncwarp();
+    // every copy issued has landed before the CTA can exit
+    if (lane == 0)
+      for (int s = 0; s < NS; ++s)
+        if (((any >> s) & 1u) && !mbar_wait_timed(&C->full[s], (last_par >> s) & 1u, limit))
+          cache_error(p, abort, CERR_DRAIN);
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ MMA issue
+      constexpr uint32_t IDESC_S = idesc_f32acc(0, 0, 128, N);
+      constexpr uint32_t IDESC_O = idesc_f32acc(0, 0, 128, N) | (1u << 15) | (1u << 16);  // V and P MN-major
+      constexpr uint32_t SW = D == 128 ? 2 : 4, ATOM = 8 * D;  // 8 rows of D bytes
+      const uint32_t kva = smem_u32(kv_s), qa = smem_u32(q_s), pa = smem_u32(p_s);
+      uint32_t n_unit = 0;
+      int vslot = 0, vpar = 0;
+      bool stop = false;
+      for (long long t = 0; t <= n_tiles && !stop; ++t) {
+        int next_v = 0, next_par = 0;
+        if (t < n_tiles) {
+          const int ds = static_cast<int>(t % C_ND);
+          if (!mbar_wait_bounded(&C->d_full[ds], static_cast<uint32_t>(t / C_ND) & 1u, abort, limit)) {
+            cache_error(p, abort, CERR_DESC);
+            break;
+          }
+          const int flags = C->desc[ds].flags;
+          next_v = C->desc[ds].vslot;
+          next_par = C->desc[ds].vparity;
+          mbar_arrive(&C->d_empty[ds]);
+          // the K tile lies one slot before its V tile, in the same turn of the ring or the last one
+          const int kslot = next_v == 0 ? NS - 1 : next_v - 1;
+          const uint32_t kpar = next_v == 0 ? next_par ^ 1 : next_par;
+          const uint32_t sb = t & 1, ph = static_cast<uint32_t>(t >> 1) & 1u;
+          if (flags & F_FIRST) {
+            ++n_unit;
+            if (!mbar_wait_bounded(&C->q_full[(n_unit - 1) & 1], ((n_unit - 1) >> 1) & 1u, abort, limit)) {
+              cache_error(p, abort, CERR_Q);
+              break;
+            }
+          }
+          if (!mbar_wait_bounded(&C->full[kslot], kpar, abort, limit) ||
+              !mbar_wait_bounded(&C->s_empty[sb], ph ^ 1u, abort, limit)) {
+            cache_error(p, abort, CERR_FULL);
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ka = kva + kslot * Sh::SLOT, qb = qa + ((n_unit - 1) & 1) * Sh::Q;
+#pragma unroll
+          for (int term = 0; term < TERMS; ++term)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              mma_f8(tmem + sb * N, sdesc(ka + kk * 32, 16, ATOM, SW), sdesc(qb + term * N * D + kk * 32, 16, ATOM, SW),
+                     IDESC_S, (term | kk) != 0);
+          mma_commit(&C->empty[kslot]);
+          mma_commit(&C->s_full[sb]);
+          if (flags & F_LAST) mma_commit(&C->q_empty[(n_unit - 1) & 1]);
+        }
+        if (t > 0) {
+          const uint32_t ob = (t - 1) & 1, ph = static_cast<uint32_t>((t - 1) >> 1) & 1u;
+          if (!mbar_wait_bounded(&C->full[vslot], vpar, abort, limit) ||
+              !mbar_wait_bounded(&C->p_full[ob], ph, abort, limit) ||
+              !mbar_wait_bounded(&C->o_empty[ob], ph ^ 1u, abort, limit)) {
+            cache_error(p, abort, CERR_P);
+            break;
+          }
+          tc_fence_after();
+          const uint32_t va = kva + vslot * Sh::SLOT, pb = pa + ob * Sh::P;
+          // 32 tokens a step.  With D = 64 the upper half of M reads the next
+          // 8-token group (LBO = one atom): lanes 64-127 hold nothing of use.
+#pragma unroll
+          for (int term = 0; term < TERMS; ++term)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f8(tmem + (2 + ob) * N, sdesc(va + kk * 32 * D, ATOM, ATOM, SW),
+                     sdesc(pb + term * N * C_TILE + kk * 512, 128, 2048, 0), IDESC_O, (term | kk) != 0);
+          mma_commit(&C->empty[vslot]);
+          mma_commit(&C->o_full[ob]);
+        }
+        vslot = next_v;
+        vpar = next_par;
+      }
+      mma_commit(&C->done);
+      if (!mbar_wait_timed(&C->done, 0, limit)) cache_error(p, abort, CERR_DRAIN);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ queries into e4m3 terms
+    uint32_t n_unit = 0;
+    for (long long t = 0; t < n_tiles; ++t) {
+      const int ds = static_cast<int>(t % C_ND);
+      if (!mbar_wait_bounded(&C->d_full[ds], static_cast<uint32_t>(t / C_ND) & 1u, abort, limit)) {
+        if (lane == 0) cache_error(p, abort, CERR_DESC);
+        break;
+      }
+      const TileDesc& d = C->desc[ds];
+      const int flags = d.flags, b = d.b, h = d.h, row0 = d.row0, rows = d.rows;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C->d_empty[ds]);
+      if (!(flags & F_FIRST)) continue;
+      const uint32_t qb = n_unit & 1;
+      if (!mbar_wait_bounded(&C->q_empty[qb], ((n_unit >> 1) & 1u) ^ 1u, abort, limit)) {
+        if (lane == 0) cache_error(p, abort, CERR_Q);
+        break;
+      }
+      ++n_unit;
+      const long long len = p.lens[b];
+      constexpr int E = D / 32;  // dims of a lane
+#pragma unroll 4
+      for (int r = warp - 2; r < rows; r += 2) {
+        const int row = row0 + r, i = row / p.G, g = row % p.G;
+        const size_t at = (((static_cast<size_t>(b) * p.L + i) * p.H) + h * p.G + g) * D + lane * E;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (HALF) {
+          const __half2* s = reinterpret_cast<const __half2*>(p.q + at * 2);
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            const float2 f = __half22float2(s[e]);
+            v[2 * e] = f.x;
+            v[2 * e + 1] = f.y;
+          }
+        } else {
+          const __nv_bfloat162* s = reinterpret_cast<const __nv_bfloat162*>(p.q + at * 2);
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            const float2 f = __bfloat1622float2(s[e]);
+            v[2 * e] = f.x;
+            v[2 * e + 1] = f.y;
+          }
+        }
+        const float amax = warp_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
+        // 2^x, so that amax / 2^x is in [224, 448]: the exponent as it stands in a float
+        const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - ((__float_as_uint(amax) & 0x7FFFFFu) > 0x600000u ? 7 : 8);
+        const int exb = min(max(ex, 1), 253);
+        const float sc = __uint_as_float(static_cast<uint32_t>(exb) << 23);
+        const float inv = __uint_as_float(static_cast<uint32_t>(254 - exb) << 23);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= inv;
+        // rows of D bytes, 16-byte chunks swizzled within 8-row atoms
+        const int byte = lane * E;
+        const int chunk = D == 128 ? (byte >> 4) ^ (r & 7) : (byte >> 4) ^ ((r >> 1) & 3);
+        uint8_t* dst = q_s + qb * Sh::Q + r * D + chunk * 16 + (byte & 15);
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term) {
+          const uint32_t c = e4m3x4(v[0], v[1], v[2], v[3]);
+          if constexpr (E == 4) *reinterpret_cast<uint32_t*>(dst + term * N * D) = c;
+          else *reinterpret_cast<uint16_t*>(dst + term * N * D) = static_cast<uint16_t>(c);
+          take_off(v, c);
+        }
+        if (lane == 0) {
+          const long long pos = len - p.L + i;
+          const int ps = static_cast<int>(pos < 0 ? -1 : pos);
+          // e4m3 has no infinity: a row that holds one scores NaN
+          C->qs[qb][r] = amax <= 3.402823466e38f ? sc * p.scale_log2 : __int_as_float(0x7fc00000);
+          C->pos[qb][r] = ps;
+          C->low[qb][r] = p.window && p.window <= ps ? ps - p.window : -1;
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read by the MMA
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C->q_full[qb]);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int half = (warp - 4) >> 2, quad = warp & 3, c0 = half * HC;
+    const int me = quad * 32 + lane;  // the token of a tile, and the dim of O
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const float ninf = -__int_as_float(0x7f800000);
+    const int page_of = me / p.page;
+    float m[HC], l[HC], acc[HC];
+    uint32_t n_unit = 0, n_x = 0;
+    int prev_tok0 = 0;
+
+    // all eight warps meet (bounded)
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C->xbar);
+      const bool got = mbar_wait_bounded(&C->xbar, n_x & 1u, abort, limit);
+      ++n_x;
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        if (lane == 0) cache_error(p, abort, CERR_X);
+        return false;
+      }
+      return true;
+    };
+    // joins tile j's O into the state
+    auto join = [&](long long j, int qb, int tok0) -> bool {
+      const uint32_t ob = j & 1, ph = static_cast<uint32_t>(j >> 1) & 1u;
+      const bool got = mbar_wait_bounded(&C->o_full[ob], ph, abort, limit);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        if (lane == 0) cache_error(p, abort, CERR_O);
+        return false;
+      }
+      tc_fence_after();
+      float o[HC];
+      tmem_ld<HC>(tmem + lanes + (2 + ob) * N + c0, o);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C->o_empty[ob]);
+#pragma unroll
+      for (int c = 0; c < HC; ++c) {
+        const float2 f = C->ab[ob][c0 + c];
+        acc[c] = fmaf(o[c], f.y, acc[c] * f.x);
+      }
+      if (C->nan_tile[ob] == static_cast<int>(j) && me < D) {
+        // a value that is NaN reaches the rows that see its token, in its dim
+#pragma unroll 1
+        for (int k = 0; k < C_TILE; ++k)
+          if ((C->nan_bits[ob][k][me >> 5] >> (me & 31)) & 1u) {
+            const int tok = tok0 + k;
+#pragma unroll
+            for (int c = 0; c < HC; ++c)
+              if (tok <= C->pos[qb][c0 + c] && (tok > C->low[qb][c0 + c] || tok < p.n_sink))
+                acc[c] = __int_as_float(0x7fc00000);
+          }
+      }
+      return true;
+    };
+
+    for (long long t = 0; t < n_tiles; ++t) {
+      const int ds = static_cast<int>(t % C_ND);
+      bool got = mbar_wait_bounded(&C->d_full[ds], static_cast<uint32_t>(t / C_ND) & 1u, abort, limit);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        if (lane == 0) cache_error(p, abort, CERR_DESC);
+        break;
+      }
+      const TileDesc& d = C->desc[ds];
+      const int flags = d.flags, tok0 = d.tok0;
+      const float ks = d.ks[page_of], rv = d.rv[page_of], vref = d.vref;
+      if (flags & F_FIRST) {
+        ++n_unit;
+        got = mbar_wait_bounded(&C->q_full[(n_unit - 1) & 1], ((n_unit - 1) >> 1) & 1u, abort, limit);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          if (lane == 0) cache_error(p, abort, CERR_Q);
+          break;
+        }
+#pragma unroll
+        for (int c = 0; c < HC; ++c) {
+          m[c] = ninf;
+          l[c] = 0.f;
+          acc[c] = 0.f;
+        }
+      }
+      const int qb = (n_unit - 1) & 1;
+      const uint32_t sb = t & 1, ph = static_cast<uint32_t>(t >> 1) & 1u;
+      got = mbar_wait_bounded(&C->s_full[sb], ph, abort, limit);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        if (lane == 0) cache_error(p, abort, CERR_S);
+        break;
+      }
+      tc_fence_after();
+      float s[HC];
+      tmem_ld<HC>(tmem + lanes + sb * N + c0, s);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C->s_empty[sb]);
+#pragma unroll
+      for (int c = 0; c < HC; ++c) s[c] *= C->qs[qb][c0 + c] * ks;
+      if (flags & F_MASK) {
+        const int tok = tok0 + me;
+        const bool there = (d.pages >> page_of) & 1;
+#pragma unroll
+        for (int c = 0; c < HC; ++c) {
+          const bool see = there && tok <= C->pos[qb][c0 + c] && (tok > C->low[qb][c0 + c] || tok < p.n_sink);
+          s[c] = see ? s[c] : ninf;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < HC; ++c) {
+        const float w = warp_max(s[c]);
+        if (lane == 0) C->red[sb][c0 + c][quad] = w;
+      }
+      if (!meet()) break;
+      float pr[HC];
+#pragma unroll
+      for (int c = 0; c < HC; ++c) {
+        const float4 r = *reinterpret_cast<const float4*>(C->red[sb][c0 + c]);
+        const float mt = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w));
+        const float e = ex2(s[c] - (mt == ninf ? 0.f : mt));
+        // the state's factor and the tile's: one of them is 1
+        const float f = mt == m[c] ? 1.f : ex2(-fabsf(m[c] - mt));
+        const bool up = mt > m[c];
+        const float fa = up ? f : 1.f, fb = up ? 1.f : f;
+        m[c] = fmaxf(m[c], mt);
+        l[c] = fmaf(e, fb, l[c] * fa);
+        pr[c] = e * rv;
+        if (lane == 0 && quad == 0) C->ab[sb][c0 + c] = make_float2(fa, fb * vref * (1.f / 256.f));
+      }
+      // P's terms, the row of a token contiguous along N in groups of 16
+#pragma unroll
+      for (int c = 0; c < HC; c += 4) {
+        float v[4] = {pr[c], pr[c + 1], pr[c + 2], pr[c + 3]};
+        const int col = c0 + c;
+        uint8_t* dst = p_s + sb * Sh::P + (col >> 4) * 2048 + me * 16 + (col & 15);
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term) {
+          const uint32_t q = e4m3x4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<uint32_t*>(dst + term * N * C_TILE) = q;
+          if (term + 1 < TERMS) take_off(v, q);
+        }
+      }
+      if (flags & F_MASK) {
+        // Values of tokens that no row sees may hold anything; 0 * NaN would
+        // reach the sums.  They are cleared; of tokens that some rows see, NaN
+        // codes are cleared and noted.
+        const long long tok = static_cast<long long>(tok0) + me;
+        const bool any = tok <= d.p_hi && (!p.window || tok > static_cast<long long>(d.p_lo) - p.window || tok < p.n_sink);
+        const bool all = tok <= d.p_lo && (!p.window || tok > static_cast<long long>(d.p_hi) - p.window || tok < p.n_sink);
+        got = mbar_wait_bounded(&C->full[d.vslot], d.vparity, abort, limit);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          if (lane == 0) cache_error(p, abort, CERR_FULL);
+          break;
+        }
+        // each half of the warps takes half of the row (no other thread touches it; order of chunks is of no matter)
+        uint4* row = reinterpret_cast<uint4*>(kv_s + d.vslot * Sh::SLOT + me * D);
+        uint32_t bits[2] = {0, 0};
+        if (!any) {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) row[half * (D / 32) + i] = make_uint4(0, 0, 0, 0);
+        } else if (!all) {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            // chunk i of the row's half, wherever the swizzle put it
+            const int chunk = half * (D / 32) + i;
+            const int at = D == 128 ? chunk ^ (me & 7) : chunk ^ ((me >> 1) & 3);
+            uint4 x = row[at];
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            bool hit = false;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (((w[q] >> (8 * e)) & 0x7Fu) == 0x7Fu) {
+                  const int bit = i * 16 + q * 4 + e;
+                  bits[bit >> 5] |= 1u << (bit & 31);
+                  w[q] &= ~(0xFFu << (8 * e));
+                  hit = true;
+                }
+            if (hit) row[at] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (p.L > 1) {
+          // bits of dims [half * D / 2, ...): two words with D = 128, one with D = 64
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) C->nan_bits[sb][me][half * (D / 64) + i] = bits[i];
+          if (bits[0] | bits[1]) C->nan_tile[sb] = static_cast<int>(t);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // P (and cleared values) are read by the MMA
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C->p_full[sb]);
+      if (!(flags & F_FIRST) && !join(t - 1, qb, prev_tok0)) break;
+      prev_tok0 = tok0;
+      if (flags & F_LAST) {
+        // the sums over the tokens, then the unit's rows or a partial result
+        if (!meet()) break;  // ab of this tile is visible
+        if (!join(t, qb, tok0)) break;
+#pragma unroll
+        for (int c = 0; c < HC; ++c) {
+          float v = l[c];
+#pragma unroll
+          for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+          if (lane == 0) C->sum[c0 + c][quad] = v;
+        }
+        if (!meet()) break;
+        const int b = d.b, h = d.h, row0 = d.row0, rows = d.rows;
+        const bool begins = d.seg || k0 == 0, whole = begins && d.left == 0;
+        float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + d.seg) * R * (D + 2);
+#pragma unroll
+        for (int c = 0; c < HC; ++c) {
+          const int r = c0 + c;
+          const float4 v = *reinterpret_cast<const float4*>(C->sum[r]);
+          const float sum = (v.x + v.y) + (v.z + v.w);
+          if (r < rows) {
+            if (whole) {
+              const int row = row0 + r, i = row / p.G, g = row % p.G;
+              const size_t at = (static_cast<size_t>(b) * p.L + i) * p.H + h * p.G + g;
+              const float o = acc[c] * (sum == 0.f ? 0.f : 1.f / sum);
+              if (me < D) {
+                if constexpr (HALF) reinterpret_cast<__half*>(p.out)[at * D + me] = __float2half_rn(o);
+                else reinterpret_cast<__nv_bfloat16*>(p.out)[at * D + me] = __float2bfloat16_rn(o);
+              }
+              if (me == 0 && p.lse) p.lse[at] = sum == 0.f ? ninf : (m[c] + log2f(sum)) * LN2;
+            } else {
+              if (me < D) part[r * D + me] = acc[c];
+              if (me == 0) {
+                part[R * D + r] = m[c];
+                part[R * D + R + r] = sum;
+              }
+            }
+          }
+        }
+        if (begins && !whole && me == 0 && half == 0) {
+          // the unit goes on in the next CTAs: the joining kernel starts from here
+          const long long end = C->stop - 1 + d.left;  // its last tile; CTA c holds tiles from c * total / n_cta on
+          const int last_cta = static_cast<int>(((end + 1) * n_cta - 1) / C->total);
+          p.meta[blockIdx.x] = make_int4(b, h * p.chunks + row0 / R, last_cta - static_cast<int>(blockIdx.x) + 1, d.seg);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C->q_empty[qb]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C->d_empty[ds]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, Sh::TMEM);
+}
+
+// Joins the partial results of the units that begin in CTA c and go on: a
+// block per (c, row), a thread per dim.
+template <int D, int R, bool HALF>
+__global__ void __launch_bounds__(128) cache_join_kernel(const CacheParams p) {
+  __shared__ float w[C_MAX_CTAS];
+  __shared__ float red[4];
+  const int4 u = p.meta[blockIdx.x];
+  if (u.x < 0) return;
+  const int b = u.x, h = u.y / p.chunks, row0 = (u.y % p.chunks) * R, n = u.z, r = blockIdx.y;
+  if (row0 + r >= p.L * p.G) return;
+  const int tid = threadIdx.x, lane = tid & 31;
+  constexpr size_t SLOT = static_cast<size_t>(R) * (D + 2);
+  const float* first = p.part + (static_cast<size_t>(blockIdx.x) * 2 + u.w) * SLOT;
+  const float* rest = p.part + static_cast<size_t>(blockIdx.x) * 2 * SLOT;  // CTA c + s, slot 0
+  float mx = -__int_as_float(0x7f800000);
+  for (int s = tid; s < n; s += 128) {
+    const float m = (s ? rest + 2 * s * SLOT : first)[R * D + r];
+    w[s] = m;
+    mx = fmaxf(mx, m);
+  }
+  mx = warp_max(mx);
+  if (lane == 0) red[tid >> 5] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  __syncthreads();
+  float sum = 0.f;
+  for (int s = tid; s < n; s += 128) {
+    const float f = w[s] == mx ? 1.f : ex2(w[s] - mx);
+    w[s] = f;
+    sum = fmaf(f, (s ? rest + 2 * s * SLOT : first)[R * D + R + r], sum);
+  }
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) red[tid >> 5] = sum;
+  __syncthreads();
+  sum = (red[0] + red[1]) + (red[2] + red[3]);
+  const int row = row0 + r, i = row / p.G, g = row % p.G;
+  const size_t at = (static_cast<size_t>(b) * p.L + i) * p.H + h * p.G + g;
+  if (tid < D) {
+    float acc = w[0] * first[r * D + tid];
+#pragma unroll 8
+    for (int s = 1; s < n; ++s) acc = fmaf(w[s], rest[2 * s * SLOT + r * D + tid], acc);
+    const float o = acc * (sum == 0.f ? 0.f : 1.f / sum);
+    if constexpr (HALF) reinterpret_cast<__half*>(p.out)[at * D + tid] = __float2half_rn(o);
+    else reinterpret_cast<__nv_bfloat16*>(p.out)[at * D + tid] = __float2bfloat16_rn(o);
+  }
+  if (tid == 0 && p.lse) p.lse[at] = sum == 0.f ? -__int_as_float(0x7f800000) : (mx + log2f(sum)) * LN2;
+}
+
+template <int D, int R, bool HALF>
+si_status launch_cache(CacheParams& p, const si_cache* c, int n_sm, const si_options* opt, cudaStream_t stream) {
+  using Sh = CacheShape<D, R, HALF>;
+  CUtensorMap tm_k, tm_v;
+  p.rows_total = static_cast<long long>(c->n_pages) * c->H_kv * c->page;
+  const uint64_t dims[2] = {D, static_cast<uint64_t>(p.rows_total)}, stride = D;
+  const uint32_t box[2] = {D, static_cast<uint32_t>(c->page)};
+  si_status st = encode_tmap(&tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c->k_pages, dims, &stride, box, D);
+  if (st == SI_OK) st = encode_tmap(&tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c->v_pages, dims, &stride, box, D);
+  if (st != SI_OK) return st;
+  p.chunks = (p.L * p.G + R - 1) / R;
+  // the tiles that a sequence can have at most
+  const long long cap = (static_cast<long long>(p.max_pages) * p.page + C_TILE - 1) / C_TILE;
+  long long tiles = cap;
+  if (p.window)
+    tiles = std::min(cap, (static_cast<long long>(p.window) + p.L + C_TILE - 2) / C_TILE + 1 +
+                              (static_cast<long long>(p.n_sink) + C_TILE - 1) / C_TILE);
+  p.cut = tiles > C_WHOLE;
+  const long long units = static_cast<long long>(p.B) * p.H_kv * p.chunks;
+  const long long most = std::min(n_sm * Sh::CTAS, C_MAX_CTAS);
+  const int grid = static_cast<int>(p.cut ? most : std::min(units, most));
+  void* own = nullptr;
+  if (p.cut) {
+    const size_t need = static_cast<size_t>(grid) * (sizeof(int4) + 2 * sizeof(float) * R * (D + 2));
+    void* ws = opt && opt->workspace && opt->workspace_bytes >= need && aligned(opt->workspace, 16) ? opt->workspace : nullptr;
+    if (!ws) {
+      st = scratch_alloc(&own, need, stream, "cache attention partial results");
+      if (st != SI_OK) return st;
+      ws = own;
+    }
+    p.meta = static_cast<int4*>(ws);
+    p.part = reinterpret_cast<float*>(p.meta + grid);
+  }
+  const size_t smem = 1024 + Sh::SLOTS * Sh::SLOT + 2 * (Sh::Q + Sh::P) + sizeof(CacheCtrl<D, R, HALF>);
+  static_assert(1024 + Sh::SLOTS * Sh::SLOT + 2 * (Sh::Q + Sh::P) + sizeof(CacheCtrl<D, R, HALF>) <=
+                    (Sh::CTAS == 2 ? 113 * 1024 : 227 * 1024), "shared memory of a CTA");
+  cudaError_t e = cudaFuncSetAttribute(cache_attention_kernel<D, R, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e == cudaSuccess) {
+    cache_attention_kernel<D, R, HALF><<<grid, C_THREADS, smem, stream>>>(tm_k, tm_v, p);
+    if (p.cut) cache_join_kernel<D, R, HALF><<<dim3(grid, std::min(R, p.L * p.G)), 128, 0, stream>>>(p);
+    e = cudaGetLastError();
+  }
+  if (own) cudaFreeAsync(own, stream);
+  return e == cudaSuccess ? SI_OK : cuda_fail(e, "cache_attention_kernel launch");
+}
+
+template <int D, bool HALF>
+si_status launch_cache_rows(CacheParams& p, const si_cache* c, int n_sm, const si_options* opt, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(p.L) * p.G;
+  if (rows <= 8) return launch_cache<D, 8, HALF>(p, c, n_sm, opt, stream);
+  if (rows <= 16) return launch_cache<D, 16, HALF>(p, c, n_sm, opt, stream);
+  if (rows <= 32) return launch_cache<D, 32, HALF>(p, c, n_sm, opt, stream);
+  return launch_cache<D, 64, HALF>(p, c, n_sm, opt, stream);
+}
+
+}  // namespace
 
 si_status check_attention(const void* q, const void* out, const float* lse, int B, int L, int H, int H_kv, int D,
                           float scale, int dtype, int n_sink) {
@@ -134,7 +977,7 @@ si_status check_attention(const void* q, const void* out, const float* lse, int 
   return SI_OK;
 }
 
-}  // namespace
+
 }  // namespace si
 
 using namespace si;
@@ -155,58 +998,47 @@ si_status si_cache_attention(const void* q, const si_cache* c, const int32_t* ta
   int* err = nullptr;
   st = error_word(opt, &err);
   if (st != SI_OK) return st;
-  RowParams p = {};
+  if (static_cast<long long>(max_pages) * c->page > 0x7FFFFFFFll - 2 * C_TILE)
+    return fail(SI_ERR_UNSUPPORTED, "max_pages * page must stay below 2^31 - %d", 2 * C_TILE);
+  int dev = 0, n_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  CacheParams p = {};
   p.q = static_cast<const uint8_t*>(q);
-  p.k = static_cast<const uint8_t*>(c->k_pages);
-  p.v = static_cast<const uint8_t*>(c->v_pages);
   p.ks = c->k_scale;
   p.vs = c->v_scale;
   p.table = table;
   p.lens = lens;
   p.out = static_cast<uint8_t*>(out);
   p.lse = lse;
+  p.err = err;
   p.B = B;
   p.L = L;
   p.H = H;
   p.H_kv = c->H_kv;
+  p.G = H / c->H_kv;
   p.page = c->page;
   p.max_pages = max_pages;
   p.n_pages = c->n_pages;
   p.window = window;
   p.n_sink = n_sink;
-  p.scale = scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(c->D));
-  return launch_rows<true>(p, c->D, dtype, static_cast<cudaStream_t>(stream));
+  p.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(c->D))) * LOG2E;
+  p.wait_limit_ns = kDefaultWaitLimitNs;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool half = dtype == SI_DTYPE_FP16;
+  if (c->D == 128) return half ? launch_cache_rows<128, true>(p, c, n_sm, opt, s) : launch_cache_rows<128, false>(p, c, n_sm, opt, s);
+  return half ? launch_cache_rows<64, true>(p, c, n_sm, opt, s) : launch_cache_rows<64, false>(p, c, n_sm, opt, s);
 }
 
-size_t si_cache_attention_workspace_size(int) { return 0; }
-
-si_status si_window_attention(const void* q, const void* k, const void* v, const int32_t* lens, int B, int S, int H,
-                              int H_kv, int D, int window, int n_sink, float scale, int dtype, void* out, float* lse,
-                              void* stream, const si_options* opt) {
-  if (!k || !v) return fail(SI_ERR_INVALID_ARGUMENT, "k and v must be non-null device pointers");
-  si_status st = check_attention(q, out, lse, B, S, H, H_kv, D, scale, dtype, n_sink);
-  if (st != SI_OK) return st;
-  if (window < 1) return fail(SI_ERR_INVALID_ARGUMENT, "window must be >= 1 (got %d)", window);
-  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(lens, 4))
-    return fail(SI_ERR_INVALID_ARGUMENT, "k and v must be 16-byte aligned; lens 4-byte aligned");
-  int* err = nullptr;
-  st = error_word(opt, &err);
-  if (st != SI_OK) return st;
-  RowParams p = {};
-  p.q = static_cast<const uint8_t*>(q);
-  p.k = static_cast<const uint8_t*>(k);
-  p.v = static_cast<const uint8_t*>(v);
-  p.lens = lens;
-  p.out = static_cast<uint8_t*>(out);
-  p.lse = lse;
-  p.B = B;
-  p.L = S;
-  p.H = H;
-  p.H_kv = H_kv;
-  p.window = window;
-  p.n_sink = n_sink;
-  p.scale = scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(D));
-  return launch_rows<false>(p, D, dtype, static_cast<cudaStream_t>(stream));
+size_t si_cache_attention_workspace_size(int D) {
+  // the largest of any number of rows: 64 rows and one CTA an SM
+  int dev = 0, n_sm = 0;
+  if (D < 1 || cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return static_cast<size_t>(std::min(2 * n_sm, C_MAX_CTAS)) * sizeof(int4) +
+         static_cast<size_t>(std::min(n_sm, C_MAX_CTAS)) * 2 * sizeof(float) * 64 * (static_cast<size_t>(D) + 2);
 }
 
 }  // extern "C"

@@ -11,6 +11,8 @@
 
 namespace si {
 
+constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;  // 2 s per bounded wait
+
 // Records `msg` as the calling thread's last error and returns `st`.
 si_status fail(si_status st, const char* fmt, ...);
 // Converts a CUDA runtime error into SI_ERR_CUDA with context.
@@ -38,6 +40,10 @@ si_status scratch_alloc(void** p, size_t bytes, cudaStream_t stream, const char*
 si_status encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                          uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
                          uint32_t box_outer);
+// The general form: `rank` dims (the first contiguous), the strides of the
+// others in bytes, the 128- or the 64-byte swizzle.
+si_status encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base, const uint64_t* dims,
+                      const uint64_t* stride_bytes, const uint32_t* box, int swizzle);
 // 3-D tiled tensor map (128-byte swizzle): dims[0] contiguous, strides (in
 // bytes) of dims 1 and 2 in any order.  Returns false, recording no error,
 // when the driver refuses the layout (the caller then uses 2-D boxes).
@@ -86,6 +92,9 @@ si_status launch_sparse_attention(const void* q, const void* kv, const int32_t* 
                                   float scale, void* out, float* lse, int* err, uint64_t wait_limit_ns,
                                   cudaStream_t stream);
 
+// The checks that the cache and the window attention share.
+si_status check_attention(const void* q, const void* out, const float* lse, int B, int L, int H, int H_kv, int D,
+                          float scale, int dtype, int n_sink);
 // Checks the description of a paged K/V cache.
 si_status check_cache(const si_cache* c);
 
