@@ -1,29 +1,193 @@
-// Attention of prompts through a sliding window with sinks.
+// Attention of prompts through a sliding window with sinks: whole tiles of
+// queries against the keys of their band.
 //
-// One warp per (sequence, query, head): it walks the visible keys with the
-// running maximum and sum of the softmax, every lane holding D / 32 dims.
+// out_i = sum_j softmax_j(scale q_i . k_j) v_j over the keys j <= i with
+// j > i - window or j < n_sink; lse_i the log of the sum.
+//
+// What bounds it: a query row reads and writes 4 D bytes and computes 4 D flops
+// a visible key, so up to a window of some 240 keys HBM decides, above it the
+// tensor cores and, as much, the exponentials (16 a clock and SM against 4096
+// products: a 128 x 128 tile takes 1024 clocks in either unit at D = 128).
+//
+// One CTA an SM, persistent over items, the longest first.  An item is a block
+// of positions of one sequence and key/value head, as two tiles of 128 query
+// rows: a row is (position, head), with all H / H_kv heads of a position next
+// to each other, so that shared heads share the keys that the item loads, and
+// its positions span few keys beyond the window.  Key tiles (KT keys) start at
+// the band's first key.  Per key tile and query tile:
+//   S = Q K^T      tcgen05 kind::f16, M = 128 rows, N = KT keys, into TMEM
+//   softmax        a thread a row: running maximum and sum in registers, P
+//                  rounded to the inputs' type over S in TMEM
+//   O += P V       A = P from TMEM, B = V read along dims (MN-major)
+// O stays in TMEM; it is rescaled only when a row's maximum grows by more than
+// 2^8 (P is then at most 256), which after the first tiles hardly happens.
+// The two query tiles alternate on the tensor cores, each one's softmax under
+// the other's products.  Key tiles of 64 keep two S buffers a query tile, of
+// 128 one.
+//
+// P is 0 where a key is masked, but 0 * NaN would reach the sums: two warps look
+// through the value tiles that some row does not see whole.  Values that no row
+// of the item sees (padding, later tokens) are cleared where they are not
+// finite; where some row does see one, the item is done again key by key.
+//
+// Warps: 0 TMA, 1 MMA issue, 2-3 value check, 4-7 and 8-11 softmax and
+// epilogue of the two query tiles.  Every wait is bounded; on expiry
+// SI_ERR_TIMEOUT is recorded, copies and MMAs in flight are drained and the
+// kernel exits.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
 #include "si_internal.h"
+#include "si_ptx.cuh"
 
 namespace si {
 namespace {
 
-struct RowParams {
+constexpr int W_THREADS = 384;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr int W_FEW = 16;  // up to so many sinks take a small tile of their own
+
+enum { WERR_Q = 61, WERR_K = 62, WERR_V = 63, WERR_S = 64, WERR_P = 65, WERR_O = 66, WERR_SCAN = 67, WERR_DRAIN = 68 };
+
+struct WindowParams {
   const uint8_t *q, *k, *v;
-  const float *ks, *vs;
-  const int32_t *table, *lens;
+  const int32_t* lens;
   uint8_t* out;
   float* lse;
-  int B, L, H, H_kv, page, max_pages, n_pages, window, n_sink;
-  float scale;
+  int* err;
+  int B, S, H, H_kv, G, P;  // P positions a query tile
+  int window, n_sink, blocks, wide_out;
+  long long items;
+  float scale_log2;
+  uint64_t wait_limit_ns;
 };
+
+// An item: positions p0 .. p0 + 2 P - 1 of sequence b, key/value head h.  Its
+// key tiles: n_sink_tiles over keys [0, sink_end), then main tiles from key
+// k_start on.  Query tile m uses the sinks' tiles and the main tiles [lo, hi).
+struct Item {
+  int b, h, p0, len, k_start, sink_end, sink_keys, n_sink_tiles, tiles, lo[2], hi[2];
+  __device__ __forceinline__ bool uses(int m, int u) const {
+    return hi[m] > lo[m] && (u < n_sink_tiles || (u - n_sink_tiles >= lo[m] && u - n_sink_tiles < hi[m]));
+  }
+};
+
+template <int KT>
+__device__ __forceinline__ Item item_of(const WindowParams& p, long long n) {
+  Item it;
+  const int bh = static_cast<int>(n % (p.B * p.H_kv));
+  it.b = bh / p.H_kv;
+  it.h = bh % p.H_kv;
+  it.p0 = (p.blocks - 1 - static_cast<int>(n / (p.B * p.H_kv))) * 2 * p.P;  // late positions see the most keys
+  it.len = p.lens ? min(max(p.lens[it.b], 0), p.S) : p.S;
+  it.k_start = max(0, it.p0 - p.window + 1);
+  it.sink_end = min(p.n_sink, it.k_start);
+  it.sink_keys = it.sink_end <= W_FEW ? W_FEW : KT;
+  it.n_sink_tiles = (it.sink_end + it.sink_keys - 1) / it.sink_keys;
+  const int k_end = min(it.p0 + 2 * p.P, it.len);
+  const int main_tiles = it.p0 < it.len ? (k_end - it.k_start + KT - 1) / KT : 0;
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const int a = it.p0 + m * p.P, e = min(a + p.P, it.len);
+    // (sinks that lie past k_start are seen from everywhere)
+    it.lo[m] = a < it.len && p.n_sink <= it.k_start ? (max(0, a - p.window + 1) - it.k_start) / KT : 0;
+    it.hi[m] = a < it.len ? (e - it.k_start + KT - 1) / KT : 0;
+  }
+  it.tiles = main_tiles ? main_tiles + it.n_sink_tiles : 0;
+  return it;
+}
+
+__device__ __forceinline__ void window_error(const WindowParams& p, volatile int* abort, int where) {
+  atomicCAS(p.err, 0, static_cast<int>(SI_ERR_TIMEOUT));
+  atomicCAS(p.err + 1, 0, where);
+  *abort = 1;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// 4-D tiled load: (dim, head, position, sequence).
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, uint64_t* bar, int x, int h, int s, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(h), "r"(s), "r"(b)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A's rows on the lanes, two 16-bit values a column.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// MN-major operand, 128-byte swizzle: atoms of 8 K-rows x 64 values; lbo bytes
+// between atoms along N.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+         static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* v) {
+  tmem_st16(addr, v);
+  tmem_st16(addr + 16, v + 16);
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 bytes a lane: whole sectors.
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+template <bool HALF>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (HALF) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
 
 template <bool HALF>
 __device__ __forceinline__ float load16(const uint8_t* p, size_t i) {
@@ -31,89 +195,528 @@ __device__ __forceinline__ float load16(const uint8_t* p, size_t i) {
   return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
 }
 
-__device__ __forceinline__ float load8(const uint8_t* p, size_t i) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(p[i], __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half*>(&h));
-}
-
-template <int D, bool HALF, bool PAGED>
-__global__ void __launch_bounds__(128) row_attention_kernel(const RowParams p) {
+// A row by a warp, key by key, each lane D / 32 dims: for items that hold
+// values that are not finite where some of their rows do not see them.
+template <int D, bool HALF>
+__device__ __noinline__ void row_by_keys(const WindowParams& p, const Item& it, int pos, int head) {
   constexpr int N = D / 32;
   const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(p.B) * p.L * p.H) return;
-  const int h = static_cast<int>(row % p.H);
-  const int i = static_cast<int>(row / p.H % p.L), b = static_cast<int>(row / p.H / p.L);
-  const int g = h / (p.H / p.H_kv);
-  long long len = p.lens ? p.lens[b] : p.L;
-  long long pos;
-  if (PAGED) {
-    pos = len - p.L + i;
-    len = min(len, static_cast<long long>(p.max_pages) * p.page);
-  } else {
-    len = min(max(len, 0ll), static_cast<long long>(p.L));
-    pos = i < len ? i : -1;
-  }
+  const size_t row = (static_cast<size_t>(it.b) * p.S + pos) * p.H + head;
   float q[N], acc[N], m = -INFINITY, sum = 0.f;
   for (int d = 0; d < N; ++d) {
-    q[d] = load16<HALF>(p.q, static_cast<size_t>(row) * D + d * 32 + lane);
+    q[d] = load16<HALF>(p.q, row * D + d * 32 + lane);
     acc[d] = 0.f;
   }
-  const long long stop = min(pos + 1, len);
-  long long first = p.window ? max(pos - p.window + 1, 0ll) : 0;
-  for (long long j = p.window ? 0 : first; j < stop; ++j) {
+  const int first = max(pos - p.window + 1, 0);
+  for (int j = 0; j <= pos; ++j) {
     if (j >= p.n_sink && j < first) j = first;
-    if (j >= stop) break;
-    float kv[N], vv[N];
-    if (PAGED) {
-      const int id = p.table[static_cast<size_t>(b) * p.max_pages + j / p.page];
-      if (id < 0 || id >= p.n_pages) continue;
-      const size_t ph = static_cast<size_t>(id) * p.H_kv + g, at = (ph * p.page + j % p.page) * D;
-      for (int d = 0; d < N; ++d) {
-        kv[d] = load8(p.k, at + d * 32 + lane) * p.ks[ph];
-        vv[d] = load8(p.v, at + d * 32 + lane) * p.vs[ph];
+    const size_t at = ((static_cast<size_t>(it.b) * p.S + j) * p.H_kv + it.h) * D;
+    float s = 0.f;
+    for (int d = 0; d < N; ++d) s = fmaf(q[d], load16<HALF>(p.k, at + d * 32 + lane), s);
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    s *= p.scale_log2;
+    const float mn = fmaxf(m, s), c = m == mn ? 1.f : ex2(m - mn), e = s == mn ? 1.f : ex2(s - mn);
+    m = mn;
+    sum = fmaf(sum, c, e);
+    for (int d = 0; d < N; ++d) acc[d] = fmaf(e, load16<HALF>(p.v, at + d * 32 + lane), acc[d] * c);
+  }
+  for (int d = 0; d < N; ++d) {
+    const size_t at = row * D + d * 32 + lane;
+    if (HALF) reinterpret_cast<__half*>(p.out)[at] = __float2half_rn(acc[d] / sum);
+    else reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(acc[d] / sum);
+  }
+  if (p.lse && lane == 0) p.lse[row] = (m + log2f(sum)) * LN2;
+}
+
+template <int D, int KT>
+struct WindowShape {
+  static constexpr int HALVES = D / 64;        // 128-byte column blocks of a row
+  static constexpr int QT = 128 * D * 2;       // a query tile
+  static constexpr int TILE = KT * D * 2;      // a K or V tile
+  static constexpr int NS = 65536 / TILE;      // slots of K, and of V
+  static constexpr int NSB = 128 / KT;         // S buffers of a query tile
+};
+
+template <int D, int KT>
+struct WindowCtrl {
+  using Sh = WindowShape<D, KT>;
+  uint64_t q_full, q_empty;
+  uint64_t k_full[Sh::NS], k_empty[Sh::NS], v_full[Sh::NS], v_empty[Sh::NS], v_ok[Sh::NS];
+  uint64_t s_full[2][2], p_full[2][2], o_step[2][2], o_empty[2], scanned[2], rows_done[2], done;
+  uint32_t tmem_slot;
+  int abort;
+  int again[2];  // number + 1 of an item that has to be done key by key (two items in turn)
+};
+
+// Low n bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+template <int D, bool HALF, int KT>
+__global__ void __launch_bounds__(W_THREADS, 1)
+    window_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k_few,
+                            const __grid_constant__ CUtensorMap tm_v_few, const WindowParams p) {
+  using Sh = WindowShape<D, KT>;
+  constexpr int NS = Sh::NS, NSB = Sh::NSB;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_s = smem;
+  uint8_t* k_s = q_s + 2 * Sh::QT;
+  uint8_t* v_s = k_s + NS * Sh::TILE;
+  auto* C = reinterpret_cast<WindowCtrl<D, KT>*>(v_s + NS * Sh::TILE);
+  volatile int* abort = &C->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t limit = p.wait_limit_ns;
+  if (tid == 0) {
+    mbar_init(&C->q_full, 1);
+    mbar_init(&C->q_empty, 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&C->k_full[s], 1);
+      mbar_init(&C->k_empty[s], 1);
+      mbar_init(&C->v_full[s], 1);
+      mbar_init(&C->v_empty[s], 1);
+      mbar_init(&C->v_ok[s], 2);
+    }
+    for (int m = 0; m < 2; ++m) {
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&C->s_full[m][s], 1);
+        mbar_init(&C->p_full[m][s], 4);
       }
-    } else {
-      const size_t at = ((static_cast<size_t>(b) * p.L + j) * p.H_kv + g) * D;
-      for (int d = 0; d < N; ++d) {
-        kv[d] = load16<HALF>(p.k, at + d * 32 + lane);
-        vv[d] = load16<HALF>(p.v, at + d * 32 + lane);
+      for (int s = 0; s < 2; ++s) mbar_init(&C->o_step[m][s], 1);
+      mbar_init(&C->o_empty[m], 4);
+      mbar_init(&C->scanned[m], 2);
+      mbar_init(&C->rows_done[m], 8);
+      C->again[m] = 0;
+    }
+    mbar_init(&C->done, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(&C->tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = C->tmem_slot;
+  // TMEM columns: S (and P over it) of query tile m at 128 m, O at 256 + 128 m
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ TMA
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+      uint32_t slot = 0, phase = 0, n_it = 0, any = 0, last = 0;
+      bool stop = false;
+      for (long long n = blockIdx.x; n < p.items && !stop; n += gridDim.x) {
+        const Item it = item_of<KT>(p, n);
+        if (!it.tiles) continue;
+        if (!mbar_wait_bounded(&C->q_empty, (n_it & 1u) ^ 1u, abort, limit)) {
+          window_error(p, abort, WERR_Q);
+          break;
+        }
+        ++n_it;
+        mbar_arrive_expect_tx(&C->q_full, 2 * p.P * p.G * D * 2);
+        for (int m = 0; m < 2; ++m)
+          for (int c = 0; c < Sh::HALVES; ++c)
+            tma_load_4d(q_s + m * Sh::QT + c * 16384, &tm_q, &C->q_full, c * 64, it.h * p.G, it.p0 + m * p.P, it.b);
+        for (int u = 0; u < it.tiles; ++u) {
+          const bool sink = u < it.n_sink_tiles, few = sink && it.sink_keys == W_FEW;
+          const int key0 = sink ? u * it.sink_keys : it.k_start + (u - it.n_sink_tiles) * KT;
+          const uint32_t bytes = few ? W_FEW * D * 2 : Sh::TILE;
+          for (int kv = 0; kv < 2; ++kv) {
+            uint64_t* full = kv ? &C->v_full[slot] : &C->k_full[slot];
+            if (!mbar_wait_bounded(kv ? &C->v_empty[slot] : &C->k_empty[slot], phase ^ 1u, abort, limit)) {
+              window_error(p, abort, kv ? WERR_V : WERR_K);
+              stop = true;
+              break;
+            }
+            mbar_arrive_expect_tx(full, bytes);
+            const CUtensorMap* tm = kv ? (few ? &tm_v_few : &tm_v) : (few ? &tm_k_few : &tm_k);
+            for (int c = 0; c < Sh::HALVES; ++c)
+              tma_load_4d((kv ? v_s : k_s) + slot * Sh::TILE + c * (KT * 128), tm, full, c * 64, it.h, key0, it.b);
+            any |= 1u << (slot + 16 * kv);
+            last = (last & ~(1u << (slot + 16 * kv))) | (phase << (slot + 16 * kv));
+          }
+          if (stop) break;
+          if (++slot == NS) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // every copy issued has landed before the CTA can exit
+      bool ok = !n_it || mbar_wait_timed(&C->q_full, (n_it - 1) & 1u, limit);
+      for (int s = 0; s < NS; ++s) {
+        if ((any >> s) & 1u) ok = mbar_wait_timed(&C->k_full[s], (last >> s) & 1u, limit) && ok;
+        if ((any >> (16 + s)) & 1u) ok = mbar_wait_timed(&C->v_full[s], (last >> (16 + s)) & 1u, limit) && ok;
+      }
+      if (!ok) window_error(p, abort, WERR_DRAIN);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ MMA issue
+      constexpr uint32_t FMT = HALF ? 0 : 1;
+      constexpr uint32_t IDESC_S = idesc_f32acc(FMT, FMT, 128, KT), IDESC_FEW = idesc_f32acc(FMT, FMT, 128, W_FEW);
+      constexpr uint32_t IDESC_O = idesc_f32acc(FMT, FMT, 128, D) | (1u << 16);  // V MN-major
+      const uint32_t qa = smem_u32(q_s), ka = smem_u32(k_s), va = smem_u32(v_s);
+      uint32_t kslot = 0, kphase = 0, vslot = 0, vphase = 0, n_it = 0;
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, ni[2] = {0, 0};  // S tiles, P tiles, items of a query tile
+      bool stop = false;
+      for (long long n = blockIdx.x; n < p.items && !stop; n += gridDim.x) {
+        const Item it = item_of<KT>(p, n);
+        if (!it.tiles) continue;
+        if (!mbar_wait_bounded(&C->q_full, n_it & 1u, abort, limit)) {
+          window_error(p, abort, WERR_Q);
+          break;
+        }
+        ++n_it;
+        bool begun[2] = {false, false};
+        for (int step = 0; step < it.tiles + NSB && !stop; ++step) {
+          const int u = step - NSB;  // the tile of this step's PV
+          if (u >= 0 && (!mbar_wait_bounded(&C->v_full[vslot], vphase, abort, limit) ||
+                         !mbar_wait_bounded(&C->v_ok[vslot], vphase, abort, limit))) {
+            window_error(p, abort, WERR_V);
+            stop = true;
+            break;
+          }
+          if (step < it.tiles && !mbar_wait_bounded(&C->k_full[kslot], kphase, abort, limit)) {
+            window_error(p, abort, WERR_K);
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          for (int m = 0; m < 2; ++m) {
+            if (u >= 0 && it.uses(m, u)) {
+              const uint32_t sb = np[m] % NSB;
+              if (!mbar_wait_bounded(&C->p_full[m][sb], (np[m] / NSB) & 1u, abort, limit) ||
+                  (!begun[m] && !mbar_wait_bounded(&C->o_empty[m], (ni[m] & 1u) ^ 1u, abort, limit))) {
+                window_error(p, abort, WERR_P);
+                stop = true;
+                break;
+              }
+              tc_fence_after();
+              const bool few = u < it.n_sink_tiles && it.sink_keys == W_FEW;
+              const int steps = few ? 1 : KT / 16;
+              for (int kk = 0; kk < steps; ++kk)
+                mma_f16_ts(tmem + 256 + m * 128, tmem + m * 128 + sb * KT + kk * 8,
+                           sdesc_mn(va + vslot * Sh::TILE + kk * 2048, KT * 128), IDESC_O, begun[m] || kk != 0);
+              mma_commit(&C->o_step[m][np[m] & 1]);
+              if (!begun[m]) ++ni[m];
+              begun[m] = true;
+              ++np[m];
+            }
+            if (step < it.tiles && it.uses(m, step)) {
+              const uint32_t sb = nq[m] % NSB;
+              const bool few = step < it.n_sink_tiles && it.sink_keys == W_FEW;
+              const uint32_t a = qa + m * Sh::QT, b = ka + kslot * Sh::TILE;
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_bf16(tmem + m * 128 + sb * KT, sdesc_kmajor_sw128(a + (kk >> 2) * 16384 + (kk & 3) * 32),
+                         sdesc_kmajor_sw128(b + (kk >> 2) * (KT * 128) + (kk & 3) * 32), few ? IDESC_FEW : IDESC_S,
+                         kk != 0);
+              mma_commit(&C->s_full[m][sb]);
+              ++nq[m];
+            }
+          }
+          if (stop) break;
+          if (u >= 0) {
+            mma_commit(&C->v_empty[vslot]);
+            if (++vslot == NS) {
+              vslot = 0;
+              vphase ^= 1u;
+            }
+          }
+          if (step < it.tiles) {
+            mma_commit(&C->k_empty[kslot]);
+            if (++kslot == NS) {
+              kslot = 0;
+              kphase ^= 1u;
+            }
+            if (step == it.tiles - 1) mma_commit(&C->q_empty);
+          }
+        }
+      }
+      mma_commit(&C->done);
+      if (!mbar_wait_timed(&C->done, 0, limit)) window_error(p, abort, WERR_DRAIN);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ value check
+    constexpr uint32_t EXP = HALF ? 0x7C007C00u : 0x7F807F80u;
+    uint32_t slot = 0, phase = 0, n_it = 0;
+    bool stop = false;
+    for (long long n = blockIdx.x; n < p.items && !stop; n += gridDim.x) {
+      const Item it = item_of<KT>(p, n);
+      if (!it.tiles) continue;
+      const int last = min(it.p0 + 2 * p.P, it.len) - 1;  // the item's last position
+      // the rows of the item before the last one have been written: again[] is free
+      if (!mbar_wait_bounded(&C->rows_done[n_it & 1], ((n_it >> 1) & 1u) ^ 1u, abort, limit)) {
+        if (lane == 0) window_error(p, abort, WERR_SCAN);
+        break;
+      }
+      for (int u = 0; u < it.tiles; ++u) {
+        if (!mbar_wait_bounded(&C->v_full[slot], phase, abort, limit)) {
+          if (lane == 0) window_error(p, abort, WERR_V);
+          stop = true;
+          break;
+        }
+        const bool sink = u < it.n_sink_tiles, few = sink && it.sink_keys == W_FEW;
+        const int keys = few ? W_FEW : KT;
+        const int key0 = sink ? u * it.sink_keys : it.k_start + (u - it.n_sink_tiles) * KT;
+        const int seen = sink ? it.sink_end : last + 1;  // keys from here on: seen by no row
+        // every row of both query tiles sees the whole tile
+        const bool all = key0 + keys <= seen && it.p0 + 2 * p.P <= it.len &&
+                         (sink || (key0 + keys - 1 <= it.p0 && (key0 > last - p.window || key0 + keys <= p.n_sink)));
+        if (!all) {
+          bool bad = false;
+          uint8_t* tile = v_s + slot * Sh::TILE;
+          for (int i = tid - 64; i < keys * Sh::HALVES * 8; i += 64) {
+            const int key = (i >> 3) % keys, c = (i >> 3) / keys;
+            uint4* at = reinterpret_cast<uint4*>(tile + c * (KT * 128) + key * 128) + (i & 7);
+            const uint4 x = *at;
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            bool hit = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t y = w[e] & EXP;
+              hit |= (y & 0xFFFFu) == (EXP & 0xFFFFu) || (y >> 16) == (EXP >> 16);
+            }
+            if (hit) {
+              if (key0 + key >= seen) *at = make_uint4(0, 0, 0, 0);
+              else bad = true;
+            }
+          }
+          if (bad) *reinterpret_cast<volatile int*>(&C->again[n_it & 1]) = static_cast<int>(n_it + 1);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // cleared values are read by the MMA
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C->v_ok[slot]);
+        if (++slot == NS) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+      if (lane == 0) mbar_arrive(&C->scanned[n_it & 1]);
+      ++n_it;
+    }
+  } else {
+    // ------------------------------------------------------------ softmax and epilogue of a query tile
+    const int m = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const float ninf = -__int_as_float(0x7f800000);
+    const int i_pos = row / p.G, head_of = row % p.G;
+    const bool used = row < p.P * p.G;
+    uint32_t ns = 0, n_it = 0;
+    for (long long n = blockIdx.x; n < p.items; n += gridDim.x) {
+      const Item it = item_of<KT>(p, n);
+      const int pos = it.p0 + m * p.P + i_pos;
+      const bool live = used && pos < it.len;
+      const int low = pos - p.window;  // the last key before the window
+      float mref = ninf, l = 0.f;
+      int count = 0;
+      bool fail = false;
+      for (int u = 0; u < it.tiles; ++u) {
+        if (!it.uses(m, u)) continue;
+        const uint32_t sb = ns % NSB;
+        const bool got = mbar_wait_bounded(&C->s_full[m][sb], (ns / NSB) & 1u, abort, limit);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          if (lane == 0) window_error(p, abort, WERR_S);
+          fail = true;
+          break;
+        }
+        ++ns;
+        tc_fence_after();
+        const bool sink = u < it.n_sink_tiles, few = sink && it.sink_keys == W_FEW;
+        const int key0 = sink ? u * it.sink_keys : it.k_start + (u - it.n_sink_tiles) * KT;
+        const int keys = few ? W_FEW : KT;
+        // columns c <= b and (c > a or c < e) are seen
+        const int b = !live ? -1 : sink ? it.sink_end - 1 - key0 : pos - key0;
+        const int a = sink ? -1 : low - key0, e = sink ? 0 : p.n_sink - key0;
+        const bool masked = __any_sync(0xFFFFFFFFu, !(b >= keys - 1 && (a < 0 || e >= keys)));
+        const uint32_t st = base + m * 128 + sb * KT;
+        const int chunks = few ? 1 : KT / 32;
+        auto bits = [&](int c) { return low_bits(b + 1 - 32 * c) & (~low_bits(a + 1 - 32 * c) | low_bits(e - 32 * c)); };
+        // the tile's maximum
+        float mx[4] = {ninf, ninf, ninf, ninf};
+        for (int c = 0; c < chunks; ++c) {
+          uint32_t x[32];
+          if (few) {
+            tmem_ld16(st, *reinterpret_cast<uint32_t(*)[16]>(x));
+#pragma unroll
+            for (int i = 16; i < 32; ++i) x[i] = 0xFF800000u;
+          } else {
+            tmem_ld32(st + 32 * c, x);
+          }
+          tmem_ld_wait();
+          if (masked) {
+            const uint32_t see = bits(c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], (see >> i) & 1u ? __uint_as_float(x[i]) : ninf);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
+          }
+        }
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        // a new reference where the maximum left the old one's reach
+        const bool grow = mref != ninf && mt > mref + 8.f;
+        if (count > 0 && __any_sync(0xFFFFFFFFu, grow)) {
+          // O so far, after its last product; rows that do not grow keep it
+          const bool got_o = mbar_wait_bounded(&C->o_step[m][ns & 1], ((ns - 2) >> 1) & 1u, abort, limit);  // product ns - 2
+          if (!__all_sync(0xFFFFFFFFu, got_o)) {
+            if (lane == 0) window_error(p, abort, WERR_O);
+            fail = true;
+            break;
+          }
+          tc_fence_after();
+          const float f = grow ? ex2(mref - mt) : 1.f;
+          l *= f;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[32];
+            tmem_ld32(base + 256 + m * 128 + 32 * c, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+            tmem_st32(base + 256 + m * 128 + 32 * c, x);
+          }
+        }
+        if (grow || mref == ninf) mref = mt;
+        const float off = mref == ninf ? 0.f : mref;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < chunks; ++c) {
+          uint32_t x[32];
+          if (few) {
+            tmem_ld16(st, *reinterpret_cast<uint32_t(*)[16]>(x));
+#pragma unroll
+            for (int i = 16; i < 32; ++i) x[i] = 0xFF800000u;
+          } else {
+            tmem_ld32(st + 32 * c, x);
+          }
+          tmem_ld_wait();
+          if (masked) {
+            const uint32_t see = bits(c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = (see >> i) & 1u ? x[i] : 0xFF800000u;
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float e0 = ex2(fmaf(__uint_as_float(x[i]), p.scale_log2, -off));
+            const float e1 = ex2(fmaf(__uint_as_float(x[i + 1]), p.scale_log2, -off));
+            sum[i & 3] += e0;
+            sum[(i + 1) & 3] += e1;
+            w[i >> 1] = pack2<HALF>(e0, e1);
+          }
+          // P lies over S, always behind the columns that are still to be read
+          if (few) tmem_st8(st, w);
+          else tmem_st16(st + 16 * c, w);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C->p_full[m][sb]);
+        ++count;
+      }
+      if (fail) break;
+      // ---- the item's rows
+      bool again = false;
+      if (it.tiles) {
+        bool got = mbar_wait_bounded(&C->scanned[n_it & 1], (n_it >> 1) & 1u, abort, limit);
+        if (got && count) got = mbar_wait_bounded(&C->o_step[m][(ns - 1) & 1], ((ns - 1) >> 1) & 1u, abort, limit);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          if (lane == 0) window_error(p, abort, WERR_SCAN);
+          break;
+        }
+        tc_fence_after();
+        again = *reinterpret_cast<volatile int*>(&C->again[n_it & 1]) == static_cast<int>(n_it + 1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C->rows_done[n_it & 1]);
+        ++n_it;
+      }
+      const bool write = used && pos < p.S && !(again && live);
+      const size_t at = (static_cast<size_t>(it.b) * p.S + pos) * p.H + it.h * p.G + head_of;
+      const float inv = live ? 1.f / l : 0.f;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32], w[16];
+        if (count) {
+          tmem_ld32(base + 256 + m * 128 + 32 * c, x);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+          w[i >> 1] = live ? pack2<HALF>(__uint_as_float(x[i]) * inv, __uint_as_float(x[i + 1]) * inv) : 0u;
+        if (write) {
+          uint8_t* dst = p.out + (at * D + 32 * c) * 2;
+          if (p.wide_out) {
+            store32(dst, w);
+            store32(dst + 32, w + 8);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(dst + 16 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        }
+      }
+      if (count) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C->o_empty[m]);
+      }
+      if (write && p.lse) p.lse[at] = live ? (mref + log2f(l)) * LN2 : ninf;
+      if (again) {
+        for (int r = quad; r < p.P * p.G; r += 4) {
+          const int rp = it.p0 + m * p.P + r / p.G;
+          if (rp < it.len) row_by_keys<D, HALF>(p, it, rp, it.h * p.G + r % p.G);
+        }
       }
     }
-    float s = 0.f;
-    for (int d = 0; d < N; ++d) s += q[d] * kv[d];
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    s *= p.scale;
-    const float mn = fmaxf(m, s), c = m == mn ? 1.f : __expf(m - mn), e = s == mn ? 1.f : __expf(s - mn);
-    m = mn;
-    sum = sum * c + e;
-    for (int d = 0; d < N; ++d) acc[d] = acc[d] * c + e * vv[d];
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  for (int d = 0; d < N; ++d) {
-    const size_t at = static_cast<size_t>(row) * D + d * 32 + lane;
-    if (HALF) reinterpret_cast<__half*>(p.out)[at] = __float2half_rn(acc[d] * inv);
-    else reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(acc[d] * inv);
-  }
-  if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? m + logf(sum) : -INFINITY;
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-template <bool PAGED>
-si_status launch_rows(const RowParams& p, int D, int dtype, cudaStream_t s) {
-  const long long rows = static_cast<long long>(p.B) * p.L * p.H;
-  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-  const bool half = dtype == SI_DTYPE_FP16;
-  if (D == 128) {
-    if (half) row_attention_kernel<128, true, PAGED><<<grid, 128, 0, s>>>(p);
-    else row_attention_kernel<128, false, PAGED><<<grid, 128, 0, s>>>(p);
-  } else {
-    if (half) row_attention_kernel<64, true, PAGED><<<grid, 128, 0, s>>>(p);
-    else row_attention_kernel<64, false, PAGED><<<grid, 128, 0, s>>>(p);
+template <int D, bool HALF, int KT>
+si_status launch_window(WindowParams& p, int n_sm, cudaStream_t stream) {
+  using Sh = WindowShape<D, KT>;
+  CUtensorMap tm_q, tm_k, tm_v, tm_k_few, tm_v_few;
+  const CUtensorMapDataType type = HALF ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  auto map = [&](CUtensorMap* m, const void* base, int heads, int box_heads, int box_pos) {
+    const uint64_t row = static_cast<uint64_t>(heads) * D * 2;
+    const uint64_t dims[4] = {D, static_cast<uint64_t>(heads), static_cast<uint64_t>(p.S), static_cast<uint64_t>(p.B)};
+    const uint64_t strides[3] = {D * 2, row, row * p.S};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(box_heads), static_cast<uint32_t>(box_pos), 1};
+    return encode_tmap(m, type, 4, base, dims, strides, box, 128);
+  };
+  si_status st = map(&tm_q, p.q, p.H, p.G, p.P);
+  if (st == SI_OK) st = map(&tm_k, p.k, p.H_kv, 1, KT);
+  if (st == SI_OK) st = map(&tm_v, p.v, p.H_kv, 1, KT);
+  if (st == SI_OK) st = map(&tm_k_few, p.k, p.H_kv, 1, W_FEW);
+  if (st == SI_OK) st = map(&tm_v_few, p.v, p.H_kv, 1, W_FEW);
+  if (st != SI_OK) return st;
+  constexpr size_t smem = 1024 + 2 * Sh::QT + 2 * Sh::NS * Sh::TILE + sizeof(WindowCtrl<D, KT>);
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  cudaError_t e = cudaFuncSetAttribute(window_attention_kernel<D, HALF, KT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess) {
+    const int grid = static_cast<int>(std::min<long long>(p.items, n_sm));
+    window_attention_kernel<D, HALF, KT><<<grid, W_THREADS, smem, stream>>>(tm_q, tm_k, tm_v, tm_k_few, tm_v_few, p);
+    e = cudaGetLastError();
   }
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? SI_OK : cuda_fail(e, "row_attention_kernel launch");
+  return e == cudaSuccess ? SI_OK : cuda_fail(e, "window_attention_kernel launch");
+}
+
+template <int D, bool HALF>
+si_status launch_window_tiles(WindowParams& p, int n_sm, cudaStream_t stream) {
+  // a query tile sees window + P - 1 keys
+  if (p.window + p.P <= 320) return launch_window<D, HALF, 64>(p, n_sm, stream);
+  return launch_window<D, HALF, 128>(p, n_sm, stream);
 }
 
 }  // namespace
@@ -135,21 +738,35 @@ si_status si_window_attention(const void* q, const void* k, const void* v, const
   int* err = nullptr;
   st = error_word(opt, &err);
   if (st != SI_OK) return st;
-  RowParams p = {};
+  int dev = 0, n_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  WindowParams p = {};
   p.q = static_cast<const uint8_t*>(q);
   p.k = static_cast<const uint8_t*>(k);
   p.v = static_cast<const uint8_t*>(v);
   p.lens = lens;
   p.out = static_cast<uint8_t*>(out);
   p.lse = lse;
+  p.err = err;
   p.B = B;
-  p.L = S;
+  p.S = S;
   p.H = H;
   p.H_kv = H_kv;
-  p.window = window;
-  p.n_sink = n_sink;
-  p.scale = scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(D));
-  return launch_rows<false>(p, D, dtype, static_cast<cudaStream_t>(stream));
+  p.G = H / H_kv;
+  p.P = 128 / p.G;
+  p.window = std::min(window, S);
+  p.n_sink = std::min(n_sink, S);
+  p.blocks = static_cast<int>((static_cast<long long>(S) + 2 * p.P - 1) / (2 * p.P));
+  p.items = static_cast<long long>(B) * H_kv * p.blocks;
+  p.wide_out = aligned(out, 32);
+  p.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(D))) * LOG2E;
+  p.wait_limit_ns = kDefaultWaitLimitNs;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool half = dtype == SI_DTYPE_FP16;
+  if (D == 128) return half ? launch_window_tiles<128, true>(p, n_sm, s) : launch_window_tiles<128, false>(p, n_sm, s);
+  return half ? launch_window_tiles<64, true>(p, n_sm, s) : launch_window_tiles<64, false>(p, n_sm, s);
 }
 
 }  // extern "C"
