@@ -42,6 +42,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "si_internal.h"
 #include "si_ptx.cuh"
@@ -62,8 +63,8 @@ struct WindowParams {
   float* lse;
   int* err;
   int B, S, H, H_kv, G, P;  // P positions a query tile
-  int window, n_sink, blocks, wide_out;
-  long long items;
+  int window, n_sink, blocks, wide_out, band_keys, band_sinks;
+  int items;  // B * H_kv * blocks: no more than rows
   float scale_log2;
   uint64_t wait_limit_ns;
 };
@@ -79,12 +80,12 @@ struct Item {
 };
 
 template <int KT>
-__device__ __forceinline__ Item item_of(const WindowParams& p, long long n) {
+__device__ __forceinline__ Item item_of(const WindowParams& p, int n) {
   Item it;
-  const int bh = static_cast<int>(n % (p.B * p.H_kv));
+  const int bh = n % (p.B * p.H_kv);
   it.b = bh / p.H_kv;
   it.h = bh % p.H_kv;
-  it.p0 = (p.blocks - 1 - static_cast<int>(n / (p.B * p.H_kv))) * 2 * p.P;  // late positions see the most keys
+  it.p0 = (p.blocks - 1 - n / (p.B * p.H_kv)) * 2 * p.P;  // late positions see the most keys
   it.len = p.lens ? min(max(p.lens[it.b], 0), p.S) : p.S;
   it.k_start = max(0, it.p0 - p.window + 1);
   it.sink_end = min(p.n_sink, it.k_start);
@@ -113,6 +114,33 @@ __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// Two values at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // 4-D tiled load: (dim, head, position, sequence).
@@ -233,7 +261,8 @@ struct WindowShape {
   static constexpr int HALVES = D / 64;        // 128-byte column blocks of a row
   static constexpr int QT = 128 * D * 2;       // a query tile
   static constexpr int TILE = KT * D * 2;      // a K or V tile
-  static constexpr int NS = 65536 / TILE;      // slots of K, and of V
+  static constexpr int NK = 65536 / TILE;      // K slots
+  static constexpr int NV = KT == 128 && D == 128 ? 3 : NK;  // V slots: a V tile is held until both query tiles are through with it
   static constexpr int NSB = 128 / KT;         // S buffers of a query tile
 };
 
@@ -241,7 +270,7 @@ template <int D, int KT>
 struct WindowCtrl {
   using Sh = WindowShape<D, KT>;
   uint64_t q_full, q_empty;
-  uint64_t k_full[Sh::NS], k_empty[Sh::NS], v_full[Sh::NS], v_empty[Sh::NS], v_ok[Sh::NS];
+  uint64_t k_full[Sh::NK], k_empty[Sh::NK], v_full[Sh::NV], v_empty[Sh::NV], v_ok[Sh::NV];
   uint64_t s_full[2][2], p_full[2][2], o_step[2][2], o_empty[2], scanned[2], rows_done[2], done;
   uint32_t tmem_slot;
   int abort;
@@ -257,22 +286,24 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k_few,
                             const __grid_constant__ CUtensorMap tm_v_few, const WindowParams p) {
   using Sh = WindowShape<D, KT>;
-  constexpr int NS = Sh::NS, NSB = Sh::NSB;
+  constexpr int NK = Sh::NK, NV = Sh::NV, NSB = Sh::NSB;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = smem;
   uint8_t* k_s = q_s + 2 * Sh::QT;
-  uint8_t* v_s = k_s + NS * Sh::TILE;
-  auto* C = reinterpret_cast<WindowCtrl<D, KT>*>(v_s + NS * Sh::TILE);
+  uint8_t* v_s = k_s + NK * Sh::TILE;
+  auto* C = reinterpret_cast<WindowCtrl<D, KT>*>(v_s + NV * Sh::TILE);
   volatile int* abort = &C->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint64_t limit = p.wait_limit_ns;
   if (tid == 0) {
     mbar_init(&C->q_full, 1);
     mbar_init(&C->q_empty, 1);
-    for (int s = 0; s < NS; ++s) {
+    for (int s = 0; s < NK; ++s) {
       mbar_init(&C->k_full[s], 1);
       mbar_init(&C->k_empty[s], 1);
+    }
+    for (int s = 0; s < NV; ++s) {
       mbar_init(&C->v_full[s], 1);
       mbar_init(&C->v_empty[s], 1);
       mbar_init(&C->v_ok[s], 2);
@@ -299,15 +330,17 @@ __global__ void __launch_bounds__(W_THREADS, 1)
   const uint32_t tmem = C->tmem_slot;
   // TMEM columns: S (and P over it) of query tile m at 128 m, O at 256 + 128 m
 
+  // 384 threads x 168 registers at launch = 128 x 88 + 256 x 208
+  if (warp < 4) regs_dec<88>();
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ TMA
       prefetch_tmap(&tm_q);
       prefetch_tmap(&tm_k);
       prefetch_tmap(&tm_v);
-      uint32_t slot = 0, phase = 0, n_it = 0, any = 0, last = 0;
+      uint32_t slots[2] = {0, 0}, phases[2] = {0, 0}, n_it = 0, any = 0, last = 0;  // K, V
       bool stop = false;
-      for (long long n = blockIdx.x; n < p.items && !stop; n += gridDim.x) {
+      for (int n = blockIdx.x; n < p.items && !stop; n += gridDim.x) {
         const Item it = item_of<KT>(p, n);
         if (!it.tiles) continue;
         if (!mbar_wait_bounded(&C->q_empty, (n_it & 1u) ^ 1u, abort, limit)) {
@@ -323,7 +356,9 @@ __global__ void __launch_bounds__(W_THREADS, 1)
           const bool sink = u < it.n_sink_tiles, few = sink && it.sink_keys == W_FEW;
           const int key0 = sink ? u * it.sink_keys : it.k_start + (u - it.n_sink_tiles) * KT;
           const uint32_t bytes = few ? W_FEW * D * 2 : Sh::TILE;
+#pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t slot = slots[kv], phase = phases[kv];
             uint64_t* full = kv ? &C->v_full[slot] : &C->k_full[slot];
             if (!mbar_wait_bounded(kv ? &C->v_empty[slot] : &C->k_empty[slot], phase ^ 1u, abort, limit)) {
               window_error(p, abort, kv ? WERR_V : WERR_K);
@@ -336,115 +371,132 @@ __global__ void __launch_bounds__(W_THREADS, 1)
               tma_load_4d((kv ? v_s : k_s) + slot * Sh::TILE + c * (KT * 128), tm, full, c * 64, it.h, key0, it.b);
             any |= 1u << (slot + 16 * kv);
             last = (last & ~(1u << (slot + 16 * kv))) | (phase << (slot + 16 * kv));
+            if (++slots[kv] == (kv ? NV : NK)) {
+              slots[kv] = 0;
+              phases[kv] ^= 1u;
+            }
           }
           if (stop) break;
-          if (++slot == NS) {
-            slot = 0;
-            phase ^= 1u;
-          }
         }
       }
       // every copy issued has landed before the CTA can exit
       bool ok = !n_it || mbar_wait_timed(&C->q_full, (n_it - 1) & 1u, limit);
-      for (int s = 0; s < NS; ++s) {
+      for (int s = 0; s < NK; ++s)
         if ((any >> s) & 1u) ok = mbar_wait_timed(&C->k_full[s], (last >> s) & 1u, limit) && ok;
+      for (int s = 0; s < NV; ++s)
         if ((any >> (16 + s)) & 1u) ok = mbar_wait_timed(&C->v_full[s], (last >> (16 + s)) & 1u, limit) && ok;
-      }
       if (!ok) window_error(p, abort, WERR_DRAIN);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ MMA issue
-      constexpr uint32_t FMT = HALF ? 0 : 1;
-      constexpr uint32_t IDESC_S = idesc_f32acc(FMT, FMT, 128, KT), IDESC_FEW = idesc_f32acc(FMT, FMT, 128, W_FEW);
-      constexpr uint32_t IDESC_O = idesc_f32acc(FMT, FMT, 128, D) | (1u << 16);  // V MN-major
-      const uint32_t qa = smem_u32(q_s), ka = smem_u32(k_s), va = smem_u32(v_s);
-      uint32_t kslot = 0, kphase = 0, vslot = 0, vphase = 0, n_it = 0;
-      uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, ni[2] = {0, 0};  // S tiles, P tiles, items of a query tile
-      bool stop = false;
-      for (long long n = blockIdx.x; n < p.items && !stop; n += gridDim.x) {
-        const Item it = item_of<KT>(p, n);
-        if (!it.tiles) continue;
-        if (!mbar_wait_bounded(&C->q_full, n_it & 1u, abort, limit)) {
-          window_error(p, abort, WERR_Q);
+    // ------------------------------------------------------------ MMA issue
+    // The whole warp walks the tiles and one lane issues: loop state and
+    // descriptors stay the same in all lanes, in uniform registers.
+    constexpr uint32_t FMT = HALF ? 0 : 1;
+    constexpr uint32_t IDESC_S = idesc_f32acc(FMT, FMT, 128, KT), IDESC_FEW = idesc_f32acc(FMT, FMT, 128, W_FEW);
+    constexpr uint32_t IDESC_O = idesc_f32acc(FMT, FMT, 128, D) | (1u << 16);  // V MN-major
+    const uint64_t qd = sdesc_kmajor_sw128(smem_u32(q_s)), kd = sdesc_kmajor_sw128(smem_u32(k_s));
+    const uint64_t vd = sdesc_mn(smem_u32(v_s), KT * 128);
+    uint32_t kslot = 0, kphase = 0, vslot = 0, vphase = 0, n_it = 0;
+    uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, ni[2] = {0, 0};  // S tiles, P tiles, items of a query tile
+    bool stop = false;
+    auto await = [&](uint64_t* bar, uint32_t parity, int where) {
+      const bool got = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort, limit));
+      if (!got && lane == 0) window_error(p, abort, where);
+      return got;
+    };
+    for (int n = blockIdx.x; n < p.items && !stop; n += gridDim.x) {
+      const Item it = item_of<KT>(p, n);
+      const int tiles = __reduce_max_sync(0xFFFFFFFFu, it.tiles), sinks = __reduce_max_sync(0xFFFFFFFFu, it.n_sink_tiles);
+      const bool few_sinks = __all_sync(0xFFFFFFFFu, it.sink_keys == W_FEW);
+      int from[2], to[2];  // main tiles of a query tile
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        from[m] = sinks + __reduce_max_sync(0xFFFFFFFFu, it.lo[m]);
+        to[m] = sinks + __reduce_max_sync(0xFFFFFFFFu, it.hi[m]);
+      }
+      if (!tiles) continue;
+      if (!await(&C->q_full, n_it & 1u, WERR_Q)) break;
+      ++n_it;
+      bool begun[2] = {false, false};
+      for (int step = 0; step < tiles + NSB; ++step) {
+        const int u = step - NSB;  // the tile of this step's PV
+        if (u >= 0 && !(await(&C->v_full[vslot], vphase, WERR_V) && await(&C->v_ok[vslot], vphase, WERR_V))) {
+          stop = true;
           break;
         }
-        ++n_it;
-        bool begun[2] = {false, false};
-        for (int step = 0; step < it.tiles + NSB && !stop; ++step) {
-          const int u = step - NSB;  // the tile of this step's PV
-          if (u >= 0 && (!mbar_wait_bounded(&C->v_full[vslot], vphase, abort, limit) ||
-                         !mbar_wait_bounded(&C->v_ok[vslot], vphase, abort, limit))) {
-            window_error(p, abort, WERR_V);
-            stop = true;
-            break;
-          }
-          if (step < it.tiles && !mbar_wait_bounded(&C->k_full[kslot], kphase, abort, limit)) {
-            window_error(p, abort, WERR_K);
-            stop = true;
-            break;
-          }
-          tc_fence_after();
-          for (int m = 0; m < 2; ++m) {
-            if (u >= 0 && it.uses(m, u)) {
-              const uint32_t sb = np[m] % NSB;
-              if (!mbar_wait_bounded(&C->p_full[m][sb], (np[m] / NSB) & 1u, abort, limit) ||
-                  (!begun[m] && !mbar_wait_bounded(&C->o_empty[m], (ni[m] & 1u) ^ 1u, abort, limit))) {
-                window_error(p, abort, WERR_P);
-                stop = true;
-                break;
-              }
-              tc_fence_after();
-              const bool few = u < it.n_sink_tiles && it.sink_keys == W_FEW;
-              const int steps = few ? 1 : KT / 16;
-              for (int kk = 0; kk < steps; ++kk)
-                mma_f16_ts(tmem + 256 + m * 128, tmem + m * 128 + sb * KT + kk * 8,
-                           sdesc_mn(va + vslot * Sh::TILE + kk * 2048, KT * 128), IDESC_O, begun[m] || kk != 0);
-              mma_commit(&C->o_step[m][np[m] & 1]);
-              if (!begun[m]) ++ni[m];
-              begun[m] = true;
-              ++np[m];
+        if (step < tiles && !await(&C->k_full[kslot], kphase, WERR_K)) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          if (u >= 0 && to[m] > from[m] && (u < sinks || (u >= from[m] && u < to[m]))) {
+            const uint32_t sb = np[m] % NSB;
+            if (!await(&C->p_full[m][sb], (np[m] / NSB) & 1u, WERR_P) ||
+                (!begun[m] && !await(&C->o_empty[m], (ni[m] & 1u) ^ 1u, WERR_P))) {
+              stop = true;
+              break;
             }
-            if (step < it.tiles && it.uses(m, step)) {
-              const uint32_t sb = nq[m] % NSB;
-              const bool few = step < it.n_sink_tiles && it.sink_keys == W_FEW;
-              const uint32_t a = qa + m * Sh::QT, b = ka + kslot * Sh::TILE;
+            tc_fence_after();
+            const uint32_t d = tmem + 256 + m * 128, a = tmem + m * 128 + sb * KT;
+            const uint64_t vs = vd + vslot * (Sh::TILE >> 4);
+            if (u < sinks && few_sinks) {
+              if (elect_one()) mma_f16_ts(d, a, vs, IDESC_O, begun[m]);
+            } else if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < KT / 16; ++kk) mma_f16_ts(d, a + kk * 8, vs + kk * (2048 >> 4), IDESC_O, begun[m] || kk != 0);
+            }
+            if (elect_one()) mma_commit(&C->o_step[m][np[m] & 1]);
+            if (!begun[m]) ++ni[m];
+            begun[m] = true;
+            ++np[m];
+          }
+          if (step < tiles && to[m] > from[m] && (step < sinks || (step >= from[m] && step < to[m]))) {
+            const uint32_t sb = nq[m] % NSB;
+            const uint32_t idesc = step < sinks && few_sinks ? IDESC_FEW : IDESC_S;
+            const uint32_t d = tmem + m * 128 + sb * KT;
+            const uint64_t a = qd + m * (Sh::QT >> 4), b = kd + kslot * (Sh::TILE >> 4);
+            if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk)
-                mma_bf16(tmem + m * 128 + sb * KT, sdesc_kmajor_sw128(a + (kk >> 2) * 16384 + (kk & 3) * 32),
-                         sdesc_kmajor_sw128(b + (kk >> 2) * (KT * 128) + (kk & 3) * 32), few ? IDESC_FEW : IDESC_S,
-                         kk != 0);
+                mma_bf16(d, a + ((kk >> 2) * 16384 + (kk & 3) * 32 >> 4), b + ((kk >> 2) * (KT * 128) + (kk & 3) * 32 >> 4),
+                         idesc, kk != 0);
               mma_commit(&C->s_full[m][sb]);
-              ++nq[m];
             }
+            ++nq[m];
           }
-          if (stop) break;
-          if (u >= 0) {
-            mma_commit(&C->v_empty[vslot]);
-            if (++vslot == NS) {
-              vslot = 0;
-              vphase ^= 1u;
-            }
+        }
+        if (stop) break;
+        if (u >= 0) {
+          if (elect_one()) mma_commit(&C->v_empty[vslot]);
+          if (++vslot == NV) {
+            vslot = 0;
+            vphase ^= 1u;
           }
-          if (step < it.tiles) {
+        }
+        if (step < tiles) {
+          if (elect_one()) {
             mma_commit(&C->k_empty[kslot]);
-            if (++kslot == NS) {
-              kslot = 0;
-              kphase ^= 1u;
-            }
-            if (step == it.tiles - 1) mma_commit(&C->q_empty);
+            if (step == tiles - 1) mma_commit(&C->q_empty);
+          }
+          if (++kslot == NK) {
+            kslot = 0;
+            kphase ^= 1u;
           }
         }
       }
+    }
+    if (elect_one()) {
       mma_commit(&C->done);
       if (!mbar_wait_timed(&C->done, 0, limit)) window_error(p, abort, WERR_DRAIN);
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------ value check
-    constexpr uint32_t EXP = HALF ? 0x7C007C00u : 0x7F807F80u;
+    constexpr uint32_t EXP = HALF ? 0x7C007C00u : 0x7F807F80u, CARRY = HALF ? 0x04000400u : 0x00800080u;
     uint32_t slot = 0, phase = 0, n_it = 0;
     bool stop = false;
-    for (long long n = blockIdx.x; n < p.items && !stop; n += gridDim.x) {
+    for (int n = blockIdx.x; n < p.items && !stop; n += gridDim.x) {
       const Item it = item_of<KT>(p, n);
       if (!it.tiles) continue;
       const int last = min(it.p0 + 2 * p.P, it.len) - 1;  // the item's last position
@@ -467,30 +519,33 @@ __global__ void __launch_bounds__(W_THREADS, 1)
         const bool all = key0 + keys <= seen && it.p0 + 2 * p.P <= it.len &&
                          (sink || (key0 + keys - 1 <= it.p0 && (key0 > last - p.window || key0 + keys <= p.n_sink)));
         if (!all) {
-          bool bad = false;
+          // a thread a key (two with 128), its row's 16-byte chunks from a
+          // place of its own on, so that the lanes meet no bank twice
           uint8_t* tile = v_s + slot * Sh::TILE;
-          for (int i = tid - 64; i < keys * Sh::HALVES * 8; i += 64) {
-            const int key = (i >> 3) % keys, c = (i >> 3) / keys;
-            uint4* at = reinterpret_cast<uint4*>(tile + c * (KT * 128) + key * 128) + (i & 7);
-            const uint4 x = *at;
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            bool hit = false;
+#pragma unroll 1
+          for (int key = tid - 64; key < keys; key += 64) {
+            uint32_t acc = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t y = w[e] & EXP;
-              hit |= (y & 0xFFFFu) == (EXP & 0xFFFFu) || (y >> 16) == (EXP >> 16);
+            for (int i = 0; i < Sh::HALVES * 8; ++i) {
+              const uint4 x = *(reinterpret_cast<const uint4*>(tile + (i >> 3) * (KT * 128) + key * 128) + ((i + key) & 7));
+              // an exponent of ones carries into the sign's place
+              acc |= ((x.x & EXP) + CARRY) | ((x.y & EXP) + CARRY) | ((x.z & EXP) + CARRY) | ((x.w & EXP) + CARRY);
             }
-            if (hit) {
-              if (key0 + key >= seen) *at = make_uint4(0, 0, 0, 0);
-              else bad = true;
+            if (acc & 0x80008000u) {
+              if (key0 + key >= seen) {
+#pragma unroll 1
+                for (int i = 0; i < Sh::HALVES * 8; ++i)
+                  *(reinterpret_cast<uint4*>(tile + (i >> 3) * (KT * 128) + key * 128) + (i & 7)) = make_uint4(0, 0, 0, 0);
+              } else {
+                *reinterpret_cast<volatile int*>(&C->again[n_it & 1]) = static_cast<int>(n_it + 1);
+              }
             }
           }
-          if (bad) *reinterpret_cast<volatile int*>(&C->again[n_it & 1]) = static_cast<int>(n_it + 1);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // cleared values are read by the MMA
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&C->v_ok[slot]);
-        if (++slot == NS) {
+        if (++slot == NV) {
           slot = 0;
           phase ^= 1u;
         }
@@ -500,13 +555,14 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax and epilogue of a query tile
+    regs_inc<208>();
     const int m = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const float ninf = -__int_as_float(0x7f800000);
     const int i_pos = row / p.G, head_of = row % p.G;
     const bool used = row < p.P * p.G;
     uint32_t ns = 0, n_it = 0;
-    for (long long n = blockIdx.x; n < p.items; n += gridDim.x) {
+    for (int n = blockIdx.x; n < p.items; n += gridDim.x) {
       const Item it = item_of<KT>(p, n);
       const int pos = it.p0 + m * p.P + i_pos;
       const bool live = used && pos < it.len;
@@ -533,85 +589,89 @@ __global__ void __launch_bounds__(W_THREADS, 1)
         const int a = sink ? -1 : low - key0, e = sink ? 0 : p.n_sink - key0;
         const bool masked = __any_sync(0xFFFFFFFFu, !(b >= keys - 1 && (a < 0 || e >= keys)));
         const uint32_t st = base + m * 128 + sb * KT;
-        const int chunks = few ? 1 : KT / 32;
         auto bits = [&](int c) { return low_bits(b + 1 - 32 * c) & (~low_bits(a + 1 - 32 * c) | low_bits(e - 32 * c)); };
-        // the tile's maximum
-        float mx[4] = {ninf, ninf, ninf, ninf};
-        for (int c = 0; c < chunks; ++c) {
-          uint32_t x[32];
-          if (few) {
-            tmem_ld16(st, *reinterpret_cast<uint32_t(*)[16]>(x));
+        // one tile of NC columns; false: a wait ran out
+        auto tile = [&](auto cols) -> bool {
+          constexpr int NC = decltype(cols)::value, CH = (NC + 31) / 32, CW = NC / CH;  // chunks of CW columns
+          float x[NC];
 #pragma unroll
-            for (int i = 16; i < 32; ++i) x[i] = 0xFF800000u;
-          } else {
-            tmem_ld32(st + 32 * c, x);
+          for (int c = 0; c < CH; ++c) {
+            if constexpr (CW == 16) tmem_ld16(st, *reinterpret_cast<uint32_t(*)[16]>(x));
+            else tmem_ld32(st + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * c));
           }
           tmem_ld_wait();
+          uint32_t none = 0;  // chunks of which no row of the warp sees anything
           if (masked) {
-            const uint32_t see = bits(c);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], (see >> i) & 1u ? __uint_as_float(x[i]) : ninf);
-          } else {
+            for (int c = 0; c < CH; ++c) {
+              const uint32_t full = CW == 16 ? 0xFFFFu : ~0u, see = bits(c) & full;
+              if (__all_sync(0xFFFFFFFFu, see == full)) continue;
+              if (__all_sync(0xFFFFFFFFu, see == 0)) none |= 1u << c;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
+              for (int i = 0; i < CW; ++i) x[CW * c + i] = (see >> i) & 1u ? x[CW * c + i] : ninf;
+            }
           }
-        }
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-        // a new reference where the maximum left the old one's reach
-        const bool grow = mref != ninf && mt > mref + 8.f;
-        if (count > 0 && __any_sync(0xFFFFFFFFu, grow)) {
-          // O so far, after its last product; rows that do not grow keep it
-          const bool got_o = mbar_wait_bounded(&C->o_step[m][ns & 1], ((ns - 2) >> 1) & 1u, abort, limit);  // product ns - 2
-          if (!__all_sync(0xFFFFFFFFu, got_o)) {
-            if (lane == 0) window_error(p, abort, WERR_O);
-            fail = true;
-            break;
-          }
-          tc_fence_after();
-          const float f = grow ? ex2(mref - mt) : 1.f;
-          l *= f;
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i < NC - 4; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], x[i + 2 * k], x[i + 2 * k + 1]);
+          mx[0] = max3(mx[0], x[NC - 4], x[NC - 3]);
+          mx[1] = max3(mx[1], x[NC - 2], x[NC - 1]);
+          const float mt = max3(max3(mx[0], mx[1], mx[2]), mx[3], ninf) * p.scale_log2;
+          // a new reference where the maximum left the old one's reach
+          const bool grow = mref != ninf && mt > mref + 8.f;
+          if (count > 0 && __any_sync(0xFFFFFFFFu, grow)) {
+            // O so far, after its last product; rows that do not grow keep it
+            const bool got_o = mbar_wait_bounded(&C->o_step[m][ns & 1], ((ns - 2) >> 1) & 1u, abort, limit);  // product ns - 2
+            if (!__all_sync(0xFFFFFFFFu, got_o)) {
+              if (lane == 0) window_error(p, abort, WERR_O);
+              return false;
+            }
+            tc_fence_after();
+            const float f = grow ? ex2(mref - mt) : 1.f;
+            l *= f;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t x[32];
-            tmem_ld32(base + 256 + m * 128 + 32 * c, x);
-            tmem_ld_wait();
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t x[32];
+              tmem_ld32(base + 256 + m * 128 + 32 * c, x);
+              tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-            tmem_st32(base + 256 + m * 128 + 32 * c, x);
+              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+              tmem_st32(base + 256 + m * 128 + 32 * c, x);
+            }
           }
+          if (grow || mref == ninf) mref = mt;
+          const float off = mref == ninf ? 0.f : mref;
+          const float2 sc = make_float2(p.scale_log2, p.scale_log2), sub = make_float2(-off, -off);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            uint32_t w[CW / 2];
+            if ((none >> c) & 1u) {
+#pragma unroll
+              for (int i = 0; i < CW / 2; ++i) w[i] = 0;
+            } else {
+#pragma unroll
+              for (int i = 0; i < CW / 2; ++i) {
+                float2 t = fma2(make_float2(x[CW * c + 2 * i], x[CW * c + 2 * i + 1]), sc, sub);
+                t = make_float2(ex2(t.x), ex2(t.y));
+                sum[i & 1] = add2(sum[i & 1], t);
+                w[i] = pack2<HALF>(t.x, t.y);
+              }
+            }
+            // P lies over S, whose columns have all been read
+            if constexpr (CW == 16) tmem_st8(st, w);
+            else tmem_st16(st + 16 * c, w);
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          return true;
+        };
+        const bool ok = few ? tile(std::integral_constant<int, W_FEW>{}) : tile(std::integral_constant<int, KT>{});
+        if (!ok) {
+          fail = true;
+          break;
         }
-        if (grow || mref == ninf) mref = mt;
-        const float off = mref == ninf ? 0.f : mref;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int c = 0; c < chunks; ++c) {
-          uint32_t x[32];
-          if (few) {
-            tmem_ld16(st, *reinterpret_cast<uint32_t(*)[16]>(x));
-#pragma unroll
-            for (int i = 16; i < 32; ++i) x[i] = 0xFF800000u;
-          } else {
-            tmem_ld32(st + 32 * c, x);
-          }
-          tmem_ld_wait();
-          if (masked) {
-            const uint32_t see = bits(c);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = (see >> i) & 1u ? x[i] : 0xFF800000u;
-          }
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float e0 = ex2(fmaf(__uint_as_float(x[i]), p.scale_log2, -off));
-            const float e1 = ex2(fmaf(__uint_as_float(x[i + 1]), p.scale_log2, -off));
-            sum[i & 3] += e0;
-            sum[(i + 1) & 3] += e1;
-            w[i >> 1] = pack2<HALF>(e0, e1);
-          }
-          // P lies over S, always behind the columns that are still to be read
-          if (few) tmem_st8(st, w);
-          else tmem_st16(st + 16 * c, w);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -680,40 +740,415 @@ __global__ void __launch_bounds__(W_THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// ------------------------------------------------------------------ narrow bands
+//
+// Where all keys of an item's two query tiles, sinks included, are at most 256
+// (window 128 with 8 heads a key/value head: 176), the whole item is one step:
+// S of a query tile takes up to 256 TMEM columns, one softmax pass needs no
+// running state, P lies over the first half of S and O over the second.  The
+// streaming form above spends its time there on the steps' hand-offs: QK
+// products of 64 columns cost as much as of 128 (the query tile has to be read
+// for either), and a query tile takes four steps.  Q, K and V have one buffer:
+// Q and K are free once both S are there, so the next item's arrive during the
+// softmax, V's during the next QK.
+//
+// Measured on window 128, 4 sinks, 64 / 8 heads, D = 128, 16,384 positions:
+// BANDFIGURES
+
+struct BandItem {
+  int b, h, p0, len, k_start, sink_end;
+};
+
+__device__ __forceinline__ BandItem band_item(const WindowParams& p, int n) {
+  BandItem it;
+  const int bh = n % (p.B * p.H_kv);
+  it.b = bh / p.H_kv;
+  it.h = bh % p.H_kv;
+  it.p0 = n / (p.B * p.H_kv) * 2 * p.P;
+  it.len = p.lens ? min(max(p.lens[it.b], 0), p.S) : p.S;
+  it.k_start = max(0, it.p0 - p.window + 1);
+  it.sink_end = min(p.n_sink, it.k_start);
+  return it;
+}
+
+constexpr int BAND_KEYS = 256;   // columns of S
+constexpr int BAND_STAGE = 4096; // a warp's rows on their way out: 32 rows x 64 dims
+
+struct BandCtrl {
+  uint64_t qk_full, qk_empty, v_full, v_empty, v_ok;
+  uint64_t s_full[2], p_full[2], o_full[2], t_empty[2], rows_done, done;
+  uint32_t tmem_slot;
+  int abort, again;
+};
+
+template <int D, bool HALF>
+__global__ void __launch_bounds__(W_THREADS, 1)
+    band_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k_sink,
+                          const __grid_constant__ CUtensorMap tm_v_sink, const WindowParams p) {
+  constexpr int HALVES = D / 64, QT = 128 * D * 2;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int keys = p.band_keys, s16 = p.band_sinks;  // columns; those of the sinks, in front
+  const int plane = keys * 128;                      // 64 dims of all keys
+  uint8_t* q_s = smem;
+  uint8_t* k_s = q_s + 2 * QT;
+  uint8_t* v_s = k_s + HALVES * plane;
+  uint8_t* o_s = v_s + HALVES * plane;
+  auto* C = reinterpret_cast<BandCtrl*>(o_s + 8 * BAND_STAGE);
+  volatile int* abort = &C->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t limit = p.wait_limit_ns;
+  if (tid == 0) {
+    mbar_init(&C->qk_full, 1);
+    mbar_init(&C->qk_empty, 1);
+    mbar_init(&C->v_full, 1);
+    mbar_init(&C->v_empty, 1);
+    mbar_init(&C->v_ok, 2);
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(&C->s_full[m], 1);
+      mbar_init(&C->p_full[m], 4);
+      mbar_init(&C->o_full[m], 1);
+      mbar_init(&C->t_empty[m], 4);
+    }
+    mbar_init(&C->rows_done, 8);
+    mbar_init(&C->done, 1);
+    *abort = 0;
+    C->again = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(&C->tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = C->tmem_slot;
+  // items of this CTA, all with the same steps: number i waits for parity i & 1
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ TMA
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+      uint32_t i = 0;
+      bool v_began = false;
+      for (int n = blockIdx.x; n < p.items; n += gridDim.x, ++i) {
+        const BandItem it = band_item(p, n);
+        if (!mbar_wait_bounded(&C->qk_empty, (i & 1u) ^ 1u, abort, limit)) {
+          window_error(p, abort, WERR_Q);
+          break;
+        }
+        mbar_arrive_expect_tx(&C->qk_full, 2 * p.P * p.G * D * 2 + keys * D * 2);
+        for (int c = 0; c < HALVES; ++c) {
+          for (int m = 0; m < 2; ++m)
+            tma_load_4d(q_s + m * QT + c * 16384, &tm_q, &C->qk_full, c * 64, it.h * p.G, it.p0 + m * p.P, it.b);
+          if (s16) tma_load_4d(k_s + c * plane, &tm_k_sink, &C->qk_full, c * 64, it.h, 0, it.b);
+          tma_load_4d(k_s + c * plane + s16 * 128, &tm_k, &C->qk_full, c * 64, it.h, it.k_start, it.b);
+        }
+        if (!mbar_wait_bounded(&C->v_empty, (i & 1u) ^ 1u, abort, limit)) {
+          window_error(p, abort, WERR_V);
+          ++i;
+          break;
+        }
+        mbar_arrive_expect_tx(&C->v_full, keys * D * 2);
+        for (int c = 0; c < HALVES; ++c) {
+          if (s16) tma_load_4d(v_s + c * plane, &tm_v_sink, &C->v_full, c * 64, it.h, 0, it.b);
+          tma_load_4d(v_s + c * plane + s16 * 128, &tm_v, &C->v_full, c * 64, it.h, it.k_start, it.b);
+        }
+        v_began = true;
+      }
+      // every copy issued has landed before the CTA can exit
+      bool ok = !i || mbar_wait_timed(&C->qk_full, (i - 1) & 1u, limit);
+      if (v_began && !*abort) ok = mbar_wait_timed(&C->v_full, (i - 1) & 1u, limit) && ok;
+      if (!ok) window_error(p, abort, WERR_DRAIN);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t FMT = HALF ? 0 : 1;
+    const uint32_t idesc_s = idesc_f32acc(FMT, FMT, 128, 0) | (static_cast<uint32_t>(keys >> 3) << 17);
+    constexpr uint32_t IDESC_O = idesc_f32acc(FMT, FMT, 128, D) | (1u << 16);  // V MN-major
+    const uint64_t qd = sdesc_kmajor_sw128(smem_u32(q_s)), kd = sdesc_kmajor_sw128(smem_u32(k_s));
+    const uint64_t vd = sdesc_mn(smem_u32(v_s), plane);
+    auto await = [&](uint64_t* bar, uint32_t parity, int where) {
+      const bool got = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort, limit));
+      if (!got && lane == 0) window_error(p, abort, where);
+      return got;
+    };
+    uint32_t i = 0;
+    bool stop = false;
+    for (int n = blockIdx.x; n < p.items && !stop; n += gridDim.x, ++i) {
+      const uint32_t par = i & 1u;
+      if (!await(&C->qk_full, par, WERR_Q)) break;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (!await(&C->t_empty[m], par ^ 1u, WERR_O)) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16(tmem + m * 256, qd + (m * QT + (kk >> 2) * 16384 + (kk & 3) * 32 >> 4),
+                     kd + ((kk >> 2) * plane + (kk & 3) * 32 >> 4), idesc_s, kk != 0);
+          mma_commit(&C->s_full[m]);
+          if (m == 1) mma_commit(&C->qk_empty);
+        }
+      }
+      if (stop || !await(&C->v_ok, par, WERR_V)) break;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (!await(&C->p_full[m], par, WERR_P)) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          for (int kk = 0; kk < keys / 16; ++kk)
+            mma_f16_ts(tmem + m * 256 + 128, tmem + m * 256 + kk * 8, vd + kk * (2048 >> 4), IDESC_O, kk != 0);
+          mma_commit(&C->o_full[m]);
+          if (m == 1) mma_commit(&C->v_empty);
+        }
+      }
+    }
+    if (elect_one()) {
+      mma_commit(&C->done);
+      if (!mbar_wait_timed(&C->done, 0, limit)) window_error(p, abort, WERR_DRAIN);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ value check
+    constexpr uint32_t EXP = HALF ? 0x7C007C00u : 0x7F807F80u, CARRY = HALF ? 0x04000400u : 0x00800080u;
+    uint32_t i = 0;
+    for (int n = blockIdx.x; n < p.items; n += gridDim.x, ++i) {
+      const BandItem it = band_item(p, n);
+      const int last = min(it.p0 + 2 * p.P, it.len) - 1;
+      // the last item's rows have been written (again is free), this one's values are here
+      const bool got = mbar_wait_bounded(&C->rows_done, (i & 1u) ^ 1u, abort, limit) &&
+                       mbar_wait_bounded(&C->v_full, i & 1u, abort, limit);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        if (lane == 0) window_error(p, abort, WERR_V);
+        break;
+      }
+#pragma unroll 1
+      for (int r = tid - 64; r < keys; r += 64) {
+        uint32_t acc = 0;
+#pragma unroll
+        for (int c = 0; c < HALVES * 8; ++c) {
+          const uint4 x = *(reinterpret_cast<const uint4*>(v_s + (c >> 3) * plane + r * 128) + ((c + r) & 7));
+          // an exponent of ones carries into the sign's place
+          acc |= ((x.x & EXP) + CARRY) | ((x.y & EXP) + CARRY) | ((x.z & EXP) + CARRY) | ((x.w & EXP) + CARRY);
+        }
+        if (acc & 0x80008000u) {
+          const bool seen = r < s16 ? r < it.sink_end : it.k_start + r - s16 <= last;
+          if (seen) {
+            *reinterpret_cast<volatile int*>(&C->again) = static_cast<int>(i + 1);
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < HALVES * 8; ++c)
+              *(reinterpret_cast<uint4*>(v_s + (c >> 3) * plane + r * 128) + (c & 7)) = make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // cleared values are read by the MMA
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C->v_ok);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax and epilogue of a query tile
+    const int m = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t st = tmem + (static_cast<uint32_t>(quad * 32) << 16) + m * 256;
+    const float ninf = -__int_as_float(0x7f800000);
+    const int i_pos = row / p.G, head_of = row % p.G;
+    const bool used = row < p.P * p.G;
+    uint8_t* stage = o_s + (warp - 4) * BAND_STAGE;
+    const int chunks = (keys + 31) / 32;
+    uint32_t i = 0;
+    for (int n = blockIdx.x; n < p.items; n += gridDim.x, ++i) {
+      const BandItem it = band_item(p, n);
+      const uint32_t par = i & 1u;
+      const int pos = it.p0 + m * p.P + i_pos;
+      const bool live = used && pos < it.len;
+      // seen: columns up to b that lie behind a, or before e; of the sinks' columns those before sink_end
+      const int b = pos - it.k_start + s16, a = b - p.window, e = p.n_sink - it.k_start + s16;
+      auto bits = [&](int c) {
+        const uint32_t main = low_bits(b + 1 - 32 * c) & (~low_bits(a + 1 - 32 * c) | low_bits(e - 32 * c)) & ~low_bits(s16 - 32 * c);
+        return live ? main | low_bits(it.sink_end - 32 * c) : 0u;
+      };
+      bool got = mbar_wait_bounded(&C->s_full[m], par, abort, limit);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        if (lane == 0) window_error(p, abort, WERR_S);
+        break;
+      }
+      tc_fence_after();
+      uint32_t some = 0;  // chunks of which some row of the warp sees something
+      float mx[4] = {ninf, ninf, ninf, ninf};
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        const uint32_t see = bits(c);
+        if (__all_sync(0xFFFFFFFFu, see == 0)) continue;
+        some |= 1u << c;
+        float x[32];
+        tmem_ld32(st + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(x));
+        tmem_ld_wait();
+        if (!__all_sync(0xFFFFFFFFu, see == ~0u)) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = (see >> k) & 1u ? x[k] : ninf;
+        }
+#pragma unroll
+        for (int k = 0; k < 32; k += 8)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], x[k + 2 * j], x[k + 2 * j + 1]);
+      }
+      const float mt = max3(max3(mx[0], mx[1], mx[2]), mx[3], ninf) * p.scale_log2;
+      const float off = mt == ninf ? 0.f : mt;
+      const float2 sc = make_float2(p.scale_log2, p.scale_log2), sub = make_float2(-off, -off);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        uint32_t w[16];
+        if ((some >> c) & 1u) {
+          const uint32_t see = bits(c);
+          float x[32];
+          tmem_ld32(st + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(x));
+          tmem_ld_wait();
+          if (!__all_sync(0xFFFFFFFFu, see == ~0u)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = (see >> k) & 1u ? x[k] : ninf;
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float2 t = fma2(make_float2(x[2 * k], x[2 * k + 1]), sc, sub);
+            t = make_float2(ex2(t.x), ex2(t.y));
+            sum[k & 1] = add2(sum[k & 1], t);
+            w[k] = pack2<HALF>(t.x, t.y);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = 0;
+        }
+        tmem_st16(st + 16 * c, w);  // behind the columns that are still to be read
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C->p_full[m]);
+      const float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      const size_t at = (static_cast<size_t>(it.b) * p.S + pos) * p.H + it.h * p.G + head_of;
+      if (p.lse && used && pos < p.S) p.lse[at] = live ? (mt + log2f(l)) * LN2 : ninf;
+      got = mbar_wait_bounded(&C->o_full[m], par, abort, limit);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        if (lane == 0) window_error(p, abort, WERR_O);
+        break;
+      }
+      tc_fence_after();
+      const bool again = *reinterpret_cast<volatile int*>(&C->again) == static_cast<int>(i + 1);
+      // 64 dims at a time through shared memory, so that whole lines go out
+      const float inv = live ? 1.f / l : 0.f;
+      const bool write = used && pos < p.S && !(again && live);
+      const uint32_t writes = __ballot_sync(0xFFFFFFFFu, write);
+#pragma unroll 1
+      for (int c = 0; c < HALVES; ++c) {
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float x[32];
+          tmem_ld32(st + 128 + c * 64 + g * 32, *reinterpret_cast<uint32_t(*)[32]>(x));
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = live ? pack2<HALF>(x[8 * j + 2 * k] * inv, x[8 * j + 2 * k + 1] * inv) : 0u;
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((g * 4 + j) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (c == HALVES - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&C->t_empty[m]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = j * 4 + (lane >> 3), ch = lane & 7;
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+          const long long to = __shfl_sync(0xFFFFFFFFu, static_cast<long long>(at), r);
+          if ((writes >> r) & 1u)
+            __stcs(reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(to) * D + c * 64) * 2) + ch, x);
+        }
+      }
+      if (again) {
+        const Item full{it.b, it.h, it.p0, it.len, 0, 0, 0, 0, 0, {0, 0}, {0, 0}};
+        for (int r = quad; r < p.P * p.G; r += 4) {
+          const int rp = it.p0 + m * p.P + r / p.G;
+          if (rp < it.len) row_by_keys<D, HALF>(p, full, rp, it.h * p.G + r % p.G);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C->rows_done);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-template <int D, bool HALF, int KT>
-si_status launch_window(WindowParams& p, int n_sm, cudaStream_t stream) {
-  using Sh = WindowShape<D, KT>;
+// Map of [B, S, heads, D] rows: boxes of 64 dims x heads x positions.
+si_status map_rows(CUtensorMap* m, bool half, const void* base, const WindowParams& p, int D, int heads, int box_heads,
+                   int box_pos) {
+  const uint64_t row = static_cast<uint64_t>(heads) * D * 2;
+  const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(heads), static_cast<uint64_t>(p.S),
+                            static_cast<uint64_t>(p.B)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, row, row * p.S};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(box_heads), static_cast<uint32_t>(box_pos), 1};
+  return encode_tmap(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides,
+                     box, 128);
+}
+
+template <typename Kernel>
+si_status launch_tiles(Kernel kernel, size_t smem, const WindowParams& p, int D, bool half, int keys, int few, int n_sm,
+                       cudaStream_t stream) {
   CUtensorMap tm_q, tm_k, tm_v, tm_k_few, tm_v_few;
-  const CUtensorMapDataType type = HALF ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  auto map = [&](CUtensorMap* m, const void* base, int heads, int box_heads, int box_pos) {
-    const uint64_t row = static_cast<uint64_t>(heads) * D * 2;
-    const uint64_t dims[4] = {D, static_cast<uint64_t>(heads), static_cast<uint64_t>(p.S), static_cast<uint64_t>(p.B)};
-    const uint64_t strides[3] = {D * 2, row, row * p.S};
-    const uint32_t box[4] = {64, static_cast<uint32_t>(box_heads), static_cast<uint32_t>(box_pos), 1};
-    return encode_tmap(m, type, 4, base, dims, strides, box, 128);
-  };
-  si_status st = map(&tm_q, p.q, p.H, p.G, p.P);
-  if (st == SI_OK) st = map(&tm_k, p.k, p.H_kv, 1, KT);
-  if (st == SI_OK) st = map(&tm_v, p.v, p.H_kv, 1, KT);
-  if (st == SI_OK) st = map(&tm_k_few, p.k, p.H_kv, 1, W_FEW);
-  if (st == SI_OK) st = map(&tm_v_few, p.v, p.H_kv, 1, W_FEW);
+  si_status st = map_rows(&tm_q, half, p.q, p, D, p.H, p.G, p.P);
+  if (st == SI_OK) st = map_rows(&tm_k, half, p.k, p, D, p.H_kv, 1, keys);
+  if (st == SI_OK) st = map_rows(&tm_v, half, p.v, p, D, p.H_kv, 1, keys);
+  if (st == SI_OK) st = map_rows(&tm_k_few, half, p.k, p, D, p.H_kv, 1, few);
+  if (st == SI_OK) st = map_rows(&tm_v_few, half, p.v, p, D, p.H_kv, 1, few);
   if (st != SI_OK) return st;
-  constexpr size_t smem = 1024 + 2 * Sh::QT + 2 * Sh::NS * Sh::TILE + sizeof(WindowCtrl<D, KT>);
-  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(window_attention_kernel<D, HALF, KT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e == cudaSuccess) {
-    const int grid = static_cast<int>(std::min<long long>(p.items, n_sm));
-    window_attention_kernel<D, HALF, KT><<<grid, W_THREADS, smem, stream>>>(tm_q, tm_k, tm_v, tm_k_few, tm_v_few, p);
+    kernel<<<std::min(p.items, n_sm), W_THREADS, smem, stream>>>(tm_q, tm_k, tm_v, tm_k_few, tm_v_few, p);
     e = cudaGetLastError();
   }
-  return e == cudaSuccess ? SI_OK : cuda_fail(e, "window_attention_kernel launch");
+  return e == cudaSuccess ? SI_OK : cuda_fail(e, "window attention launch");
+}
+
+template <int D, bool HALF, int KT>
+si_status launch_window(const WindowParams& p, int n_sm, cudaStream_t stream) {
+  using Sh = WindowShape<D, KT>;
+  constexpr size_t smem = 1024 + 2 * Sh::QT + (Sh::NK + Sh::NV) * Sh::TILE + sizeof(WindowCtrl<D, KT>);
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  return launch_tiles(window_attention_kernel<D, HALF, KT>, smem, p, D, HALF, KT, W_FEW, n_sm, stream);
 }
 
 template <int D, bool HALF>
 si_status launch_window_tiles(WindowParams& p, int n_sm, cudaStream_t stream) {
+  const long long sinks = (static_cast<long long>(p.n_sink) + 15) / 16 * 16;
+  const long long keys = sinks + (2ll * p.P + p.window - 1 + 15) / 16 * 16;
+  if (keys <= BAND_KEYS) {
+    p.band_keys = static_cast<int>(keys);
+    p.band_sinks = static_cast<int>(sinks);
+    constexpr size_t most = 1024 + 2 * 128 * D * 2 + 2 * BAND_KEYS * D * 2 + 8 * BAND_STAGE + sizeof(BandCtrl);
+    static_assert(most <= 227 * 1024, "shared memory of a CTA");
+    const size_t smem = 1024 + 2 * 128 * D * 2 + 2 * p.band_keys * D * 2 + 8 * BAND_STAGE + sizeof(BandCtrl);
+    return launch_tiles(band_attention_kernel<D, HALF>, smem, p, D, HALF, p.band_keys - p.band_sinks,
+                        std::max(p.band_sinks, 16), n_sm, stream);
+  }
   // a query tile sees window + P - 1 keys
   if (p.window + p.P <= 320) return launch_window<D, HALF, 64>(p, n_sm, stream);
   return launch_window<D, HALF, 128>(p, n_sm, stream);
@@ -759,7 +1194,7 @@ si_status si_window_attention(const void* q, const void* k, const void* v, const
   p.window = std::min(window, S);
   p.n_sink = std::min(n_sink, S);
   p.blocks = static_cast<int>((static_cast<long long>(S) + 2 * p.P - 1) / (2 * p.P));
-  p.items = static_cast<long long>(B) * H_kv * p.blocks;
+  p.items = B * H_kv * p.blocks;
   p.wide_out = aligned(out, 32);
   p.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(D))) * LOG2E;
   p.wait_limit_ns = kDefaultWaitLimitNs;
