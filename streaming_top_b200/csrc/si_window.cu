@@ -217,6 +217,15 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
+// Two packed values times f.
+template <bool HALF>
+__device__ __forceinline__ uint32_t scale2(uint32_t v, float f) {
+  float2 t;
+  if constexpr (HALF) t = __half22float2(*reinterpret_cast<const __half2*>(&v));
+  else t = make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+  return pack2<HALF>(t.x * f, t.y * f);
+}
+
 template <bool HALF>
 __device__ __forceinline__ float load16(const uint8_t* p, size_t i) {
   if (HALF) return __half2float(reinterpret_cast<const __half*>(p)[i]);
@@ -776,7 +785,7 @@ constexpr int BAND_STAGE = 4096; // a warp's rows on their way out: 32 rows x 64
 
 struct BandCtrl {
   uint64_t qk_full, qk_empty, v_full, v_empty, v_ok;
-  uint64_t s_full[2], p_full[2], o_full[2], t_empty[2], rows_done, done;
+  uint64_t s_full[2], p_full[2], o_full[2], t_empty[2], checked, done;
   uint32_t tmem_slot;
   int abort, again;
 };
@@ -811,7 +820,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       mbar_init(&C->o_full[m], 1);
       mbar_init(&C->t_empty[m], 4);
     }
-    mbar_init(&C->rows_done, 8);
+    mbar_init(&C->checked, 8);
     mbar_init(&C->done, 1);
     *abort = 0;
     C->again = 0;
@@ -922,8 +931,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     for (int n = blockIdx.x; n < p.items; n += gridDim.x, ++i) {
       const BandItem it = band_item(p, n);
       const int last = min(it.p0 + 2 * p.P, it.len) - 1;
-      // the last item's rows have been written (again is free), this one's values are here
-      const bool got = mbar_wait_bounded(&C->rows_done, (i & 1u) ^ 1u, abort, limit) &&
+      // the last item's verdict has been read, this one's values are here
+      const bool got = mbar_wait_bounded(&C->checked, (i & 1u) ^ 1u, abort, limit) &&
                        mbar_wait_bounded(&C->v_full, i & 1u, abort, limit);
       if (!__all_sync(0xFFFFFFFFu, got)) {
         if (lane == 0) window_error(p, abort, WERR_V);
@@ -961,7 +970,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     const int i_pos = row / p.G, head_of = row % p.G;
     const bool used = row < p.P * p.G;
     uint8_t* stage = o_s + (warp - 4) * BAND_STAGE;
-    const int chunks = (keys + 31) / 32;
+    const int chunks = (keys + 63) / 64;
     uint32_t i = 0;
     for (int n = blockIdx.x; n < p.items; n += gridDim.x, ++i) {
       const BandItem it = band_item(p, n);
@@ -980,53 +989,71 @@ __global__ void __launch_bounds__(W_THREADS, 1)
         break;
       }
       tc_fence_after();
-      uint32_t some = 0;  // chunks of which some row of the warp sees something
-      float mx[4] = {ninf, ninf, ninf, ninf};
-#pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        const uint32_t see = bits(c);
-        if (__all_sync(0xFFFFFFFFu, see == 0)) continue;
-        some |= 1u << c;
-        float x[32];
-        tmem_ld32(st + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(x));
-        tmem_ld_wait();
-        if (!__all_sync(0xFFFFFFFFu, see == ~0u)) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = (see >> k) & 1u ? x[k] : ninf;
-        }
-#pragma unroll
-        for (int k = 0; k < 32; k += 8)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], x[k + 2 * j], x[k + 2 * j + 1]);
-      }
-      const float mt = max3(max3(mx[0], mx[1], mx[2]), mx[3], ninf) * p.scale_log2;
-      const float off = mt == ninf ? 0.f : mt;
-      const float2 sc = make_float2(p.scale_log2, p.scale_log2), sub = make_float2(-off, -off);
+      // One pass, 64 columns at a time: P relative to a whole power of two, taken
+      // from the first columns that are seen; where a later column exceeds it by
+      // more than 2^8, what was written is scaled, which a power of two does
+      // without rounding.
+      float ref = ninf;
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      const float2 sc = make_float2(p.scale_log2, p.scale_log2);
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
-        uint32_t w[16];
-        if ((some >> c) & 1u) {
-          const uint32_t see = bits(c);
-          float x[32];
-          tmem_ld32(st + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(x));
+        const uint32_t see[2] = {bits(2 * c), bits(2 * c + 1)};
+        uint32_t w[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) w[k] = 0;
+        if (__any_sync(0xFFFFFFFFu, (see[0] | see[1]) != 0)) {
+          float x[64];
+          tmem_ld32(st + 64 * c, *reinterpret_cast<uint32_t(*)[32]>(x));
+          tmem_ld32(st + 64 * c + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
           tmem_ld_wait();
-          if (!__all_sync(0xFFFFFFFFu, see == ~0u)) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = (see >> k) & 1u ? x[k] : ninf;
+          for (int h = 0; h < 2; ++h)
+            if (!__all_sync(0xFFFFFFFFu, see[h] == ~0u)) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[32 * h + k] = (see[h] >> k) & 1u ? x[32 * h + k] : ninf;
+            }
+          float mx[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mx[j] = max3(x[j], x[8 + j], x[16 + j]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mx[j] = max3(mx[j], x[24 + j], x[32 + j]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mx[j] = max3(max3(mx[j], x[40 + j], x[48 + j]), x[56 + j], ninf);
+          const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * p.scale_log2;
+          const bool grow = ref != ninf && mt > ref + 8.f;
+          if (__any_sync(0xFFFFFFFFu, grow)) {
+            const float to = ceilf(mt), f = grow ? ex2(ref - to) : 1.f;
+            if (grow) ref = to;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) sum[k] = make_float2(sum[k].x * f, sum[k].y * f);
+#pragma unroll 1
+            for (int o = 0; o < 2 * c; ++o) {
+              uint32_t y[16];
+              tmem_ld16(st + 16 * o, y);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) y[k] = scale2<HALF>(y[k], f);
+              tmem_st16(st + 16 * o, y);
+            }
+            tmem_st_wait();
           }
+          if (ref == ninf) ref = ceilf(mt);
+          const float off = ref == ninf ? 0.f : ref;
+          const float2 sub = make_float2(-off, -off);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float2 t = fma2(make_float2(x[2 * k], x[2 * k + 1]), sc, sub);
-            t = make_float2(ex2(t.x), ex2(t.y));
-            sum[k & 1] = add2(sum[k & 1], t);
-            w[k] = pack2<HALF>(t.x, t.y);
-          }
-        } else {
+          for (int g = 0; g < 4; ++g)
+            if (__any_sync(0xFFFFFFFFu, (see[g >> 1] >> (16 * (g & 1))) & 0xFFFFu)) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) w[k] = 0;
+              for (int k = 8 * g; k < 8 * g + 8; ++k) {
+                float2 t = fma2(make_float2(x[2 * k], x[2 * k + 1]), sc, sub);
+                t = make_float2(ex2(t.x), ex2(t.y));
+                sum[k & 1] = add2(sum[k & 1], t);
+                w[k] = pack2<HALF>(t.x, t.y);
+              }
+            }
         }
-        tmem_st16(st + 16 * c, w);  // behind the columns that are still to be read
+        tmem_st32(st + 32 * c, w);  // behind the columns that are still to be read
       }
       tmem_st_wait();
       tc_fence_before();
@@ -1034,7 +1061,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       if (lane == 0) mbar_arrive(&C->p_full[m]);
       const float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       const size_t at = (static_cast<size_t>(it.b) * p.S + pos) * p.H + it.h * p.G + head_of;
-      if (p.lse && used && pos < p.S) p.lse[at] = live ? (mt + log2f(l)) * LN2 : ninf;
+      if (p.lse && used && pos < p.S) p.lse[at] = live ? (ref + log2f(l)) * LN2 : ninf;
       got = mbar_wait_bounded(&C->o_full[m], par, abort, limit);
       if (!__all_sync(0xFFFFFFFFu, got)) {
         if (lane == 0) window_error(p, abort, WERR_O);
@@ -1042,40 +1069,42 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       }
       tc_fence_after();
       const bool again = *reinterpret_cast<volatile int*>(&C->again) == static_cast<int>(i + 1);
-      // 64 dims at a time through shared memory, so that whole lines go out
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C->checked);
+      // O leaves TMEM at once, so that the next S can come; then 64 dims at a
+      // time through shared memory, so that whole lines go out
       const float inv = live ? 1.f / l : 0.f;
       const bool write = used && pos < p.S && !(again && live);
       const uint32_t writes = __ballot_sync(0xFFFFFFFFu, write);
-#pragma unroll 1
+      uint32_t w[D / 2];
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float x[32];
+        tmem_ld32(st + 128 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x));
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) w[c * 16 + k] = live ? pack2<HALF>(x[2 * k] * inv, x[2 * k + 1] * inv) : 0u;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C->t_empty[m]);
+      uint8_t* out = p.out + (static_cast<size_t>(it.b) * p.S + it.p0) * p.H * (D * 2);  // the item's first row
+      const uint32_t rel = static_cast<uint32_t>((m * p.P + i_pos) * p.H + it.h * p.G + head_of);
+#pragma unroll
       for (int c = 0; c < HALVES; ++c) {
         __syncwarp();
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float x[32];
-          tmem_ld32(st + 128 + c * 64 + g * 32, *reinterpret_cast<uint32_t(*)[32]>(x));
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = live ? pack2<HALF>(x[8 * j + 2 * k] * inv, x[8 * j + 2 * k + 1] * inv) : 0u;
-            *reinterpret_cast<uint4*>(stage + lane * 128 + (((g * 4 + j) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        if (c == HALVES - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&C->t_empty[m]);
-        }
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+              make_uint4(w[c * 32 + 4 * j], w[c * 32 + 4 * j + 1], w[c * 32 + 4 * j + 2], w[c * 32 + 4 * j + 3]);
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int r = j * 4 + (lane >> 3), ch = lane & 7;
           const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
-          const long long to = __shfl_sync(0xFFFFFFFFu, static_cast<long long>(at), r);
+          const uint32_t to = __shfl_sync(0xFFFFFFFFu, rel, r);
           if ((writes >> r) & 1u)
-            __stcs(reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(to) * D + c * 64) * 2) + ch, x);
+            __stcs(reinterpret_cast<uint4*>(out + static_cast<size_t>(to) * (D * 2) + c * 128) + ch, x);
         }
       }
       if (again) {
@@ -1085,8 +1114,6 @@ __global__ void __launch_bounds__(W_THREADS, 1)
           if (rp < it.len) row_by_keys<D, HALF>(p, full, rp, it.h * p.G + r % p.G);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&C->rows_done);
     }
   }
 
