@@ -11,8 +11,10 @@
 // lanes and the few query rows on N, so no lane of the tensor core's M is
 // padding.  q and the softmax weights, which have more bits than e4m3, enter
 // as sums of e4m3 terms (two carry 8 bits, bf16's own precision; three the 11
-// of fp16): q = 2^x (t0 + t1 [+ t2]), each term the rounded rest, accumulated
-// into the same fp32 accumulator by one more pass of the same MMA.  With x
+// of fp16): q = 2^x (t0 + t1 [+ t2]), each term the rounded rest.  The terms
+// stand side by side on N, so that the cached tile, whose reading bounds a
+// product with so few columns, is read once for all of them, and their
+// columns are added up when the accumulator is read.  With x
 // from the row's largest magnitude (224 .. 448) bf16's terms are exact down to
 // 2^-14 of it, then off by 2^-19 of it at most.  P is scaled likewise: a
 // tile's weights are taken relative to the tile's own maximum and to its
@@ -183,14 +185,15 @@ __device__ __forceinline__ void take_off(float (&v)[4], uint32_t codes) {
 // Sizes of an instantiation: R query rows of a unit (8, 16, 32 or 64).
 template <int D, int R, bool HALF>
 struct CacheShape {
-  static constexpr int N = R < 16 ? 16 : R;    // the MMAs' N
   static constexpr int TERMS = HALF ? 3 : 2;   // e4m3 terms of q and of P
+  static constexpr int N = (TERMS * R + 15) / 16 * 16;  // the MMAs' N: term i of row r is column i R + r
   static constexpr int CTAS = R <= 16 ? 2 : 1; // per SM
   static constexpr int SLOT = C_TILE * D;      // a K or V tile
-  static constexpr int Q = TERMS * N * D;      // one q buffer
-  static constexpr int P = TERMS * N * C_TILE; // one P buffer
-  static constexpr int SLOTS = CTAS == 2 ? (D == 128 ? 5 : 10) : (R == 32 || D == 64 ? 8 : 6);
-  static constexpr int TMEM = 4 * N;           // S and O, two buffers each
+  static constexpr int Q = N * D;              // one q buffer
+  static constexpr int P = N * C_TILE;         // one P buffer
+  static constexpr int SLOTS = CTAS == 2 ? (D == 128 ? 5 : 10) : (R == 32 || D == 64 ? 10 : 8);
+  static constexpr int TMEM = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 4 * N <= 256 ? 256 : 512;  // S and O, two buffers each
+  static_assert(4 * N <= 512 / CTAS, "tensor memory");
 };
 
 template <int D, int R, bool HALF>
@@ -198,11 +201,13 @@ struct CacheCtrl {
   using Sh = CacheShape<D, R, HALF>;
   uint64_t full[Sh::SLOTS], empty[Sh::SLOTS];
   uint64_t d_full[C_ND], d_empty[C_ND];
-  uint64_t q_full[2], q_empty[2], s_full[2], s_empty[2], p_full[2], o_full[2], o_empty[2], xbar, done;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], xbar, done;
+  int k_flags[Sh::SLOTS];             // flags of the tile whose keys a slot holds
   TileDesc desc[C_ND];
   alignas(16) float qs[2][R];         // score scale of a row
   alignas(16) int pos[2][R];          // a row's position; -1: sees nothing
   alignas(16) int low[2][R];          // tokens at or below are before its window
+  alignas(16) int out[2][R];          // its row of the output
   alignas(16) float red[2][R][4];     // per row and quadrant of lanes: the tile's maximum
   alignas(16) float sum[R][4];        // the same: the unit's sum
   alignas(16) float2 ab[2][R];        // per row: factors of the state and of the tile's O
@@ -239,16 +244,14 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
     }
     for (int s = 0; s < C_ND; ++s) {
       mbar_init(&C->d_full[s], 1);
-      mbar_init(&C->d_empty[s], 11);  // MMA, two q warps, eight softmax warps
+      mbar_init(&C->d_empty[s], 10);  // two q warps, eight softmax warps
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&C->q_full[s], 2);
       mbar_init(&C->q_empty[s], 9);   // the MMAs' commit, eight softmax warps
       mbar_init(&C->s_full[s], 1);
-      mbar_init(&C->s_empty[s], 8);
       mbar_init(&C->p_full[s], 8);
       mbar_init(&C->o_full[s], 1);
-      mbar_init(&C->o_empty[s], 8);
       C->nan_tile[s] = -1;
     }
     mbar_init(&C->xbar, 8);
@@ -419,7 +422,10 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
             stop = true;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(&C->full[slot], Sh::SLOT);
+          if (lane == 0) {
+            if (kv == 0) C->k_flags[slot] = d.flags;
+            mbar_arrive_expect_tx(&C->full[slot], Sh::SLOT);
+          }
           __syncwarp();
           if (gi == i) tma_load_2d(kv_s + slot * Sh::SLOT + pj * p.page * D, kv ? &tm_v : &tm_k, &C->full[slot], 0, y);
           any |= 1u << slot;
@@ -449,79 +455,70 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
         if (((any >> s) & 1u) && !mbar_wait_timed(&C->full[s], (last_par >> s) & 1u, limit))
           cache_error(p, abort, CERR_DRAIN);
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ MMA issue
-      constexpr uint32_t IDESC_S = idesc_f32acc(0, 0, 128, N);
-      constexpr uint32_t IDESC_O = idesc_f32acc(0, 0, 128, N) | (1u << 15) | (1u << 16);  // V and P MN-major
-      constexpr uint32_t SW = D == 128 ? 2 : 4, ATOM = 8 * D;  // 8 rows of D bytes
-      const uint32_t kva = smem_u32(kv_s), qa = smem_u32(q_s), pa = smem_u32(p_s);
-      uint32_t n_unit = 0;
-      int vslot = 0, vpar = 0;
-      bool stop = false;
-      for (long long t = 0; t <= n_tiles && !stop; ++t) {
-        int next_v = 0, next_par = 0;
-        if (t < n_tiles) {
-          const int ds = static_cast<int>(t % C_ND);
-          if (!mbar_wait_bounded(&C->d_full[ds], static_cast<uint32_t>(t / C_ND) & 1u, abort, limit)) {
-            cache_error(p, abort, CERR_DESC);
-            break;
-          }
-          const int flags = C->desc[ds].flags;
-          next_v = C->desc[ds].vslot;
-          next_par = C->desc[ds].vparity;
-          mbar_arrive(&C->d_empty[ds]);
-          // the K tile lies one slot before its V tile, in the same turn of the ring or the last one
-          const int kslot = next_v == 0 ? NS - 1 : next_v - 1;
-          const uint32_t kpar = next_v == 0 ? next_par ^ 1 : next_par;
-          const uint32_t sb = t & 1, ph = static_cast<uint32_t>(t >> 1) & 1u;
-          if (flags & F_FIRST) {
-            ++n_unit;
-            if (!mbar_wait_bounded(&C->q_full[(n_unit - 1) & 1], ((n_unit - 1) >> 1) & 1u, abort, limit)) {
-              cache_error(p, abort, CERR_Q);
-              break;
-            }
-          }
-          if (!mbar_wait_bounded(&C->full[kslot], kpar, abort, limit) ||
-              !mbar_wait_bounded(&C->s_empty[sb], ph ^ 1u, abort, limit)) {
-            cache_error(p, abort, CERR_FULL);
-            break;
-          }
-          tc_fence_after();
-          const uint32_t ka = kva + kslot * Sh::SLOT, qb = qa + ((n_unit - 1) & 1) * Sh::Q;
+    // ------------------------------------------------------------ MMA issue
+    // S(t) needs no wait for its TMEM buffer: P(t - 2), which has been waited
+    // for, was written after S(t - 2) had been read.  Nor does O(t - 1): a warp
+    // writes its part of P(t - 1) after it has read O(t - 3).
+    constexpr uint32_t IDESC_S = idesc_f32acc(0, 0, 128, N);
+    constexpr uint32_t IDESC_O = idesc_f32acc(0, 0, 128, N) | (1u << 15) | (1u << 16);  // V and P MN-major
+    constexpr uint32_t SW = D == 128 ? 2 : 4, ATOM = 8 * D;  // 8 rows of D bytes
+    const uint64_t kd = sdesc(smem_u32(kv_s), 16, ATOM, SW), qd = sdesc(smem_u32(q_s), 16, ATOM, SW);
+    // With D = 64 the upper half of M reads the next 8-token group (LBO = one
+    // atom): lanes 64-127 of O hold nothing of use.
+    const uint64_t vd = sdesc(smem_u32(kv_s), ATOM, ATOM, SW), pd = sdesc(smem_u32(p_s), 128, 2048, 0);
+    auto await = [&](uint64_t* bar, uint32_t parity, int where) {
+      const bool got = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort, limit));
+      if (!got && lane == 0) cache_error(p, abort, where);
+      return got;
+    };
+    uint32_t n_unit = 0, slot = 0, phase = 0, vslot = 0, vphase = 0;
+    for (long long t = 0; t <= n_tiles; ++t) {
+      uint32_t next_v = 0, next_vphase = 0;
+      if (t < n_tiles) {
+        const uint32_t sb = t & 1;
+        if (!await(&C->full[slot], phase, CERR_FULL)) break;
+        const int flags = *reinterpret_cast<volatile int*>(&C->k_flags[slot]);
+        if (flags & F_FIRST) {
+          ++n_unit;
+          if (!await(&C->q_full[(n_unit - 1) & 1], ((n_unit - 1) >> 1) & 1u, CERR_Q)) break;
+        }
+        tc_fence_after();
+        const uint64_t k = kd + slot * (Sh::SLOT >> 4), q = qd + ((n_unit - 1) & 1) * (Sh::Q >> 4);
+        if (elect_one()) {
 #pragma unroll
-          for (int term = 0; term < TERMS; ++term)
-#pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-              mma_f8(tmem + sb * N, sdesc(ka + kk * 32, 16, ATOM, SW), sdesc(qb + term * N * D + kk * 32, 16, ATOM, SW),
-                     IDESC_S, (term | kk) != 0);
-          mma_commit(&C->empty[kslot]);
+          for (int kk = 0; kk < D / 32; ++kk) mma_f8(tmem + sb * N, k + kk * 2, q + kk * 2, IDESC_S, kk != 0);
           mma_commit(&C->s_full[sb]);
+          mma_commit(&C->empty[slot]);
           if (flags & F_LAST) mma_commit(&C->q_empty[(n_unit - 1) & 1]);
         }
-        if (t > 0) {
-          const uint32_t ob = (t - 1) & 1, ph = static_cast<uint32_t>((t - 1) >> 1) & 1u;
-          if (!mbar_wait_bounded(&C->full[vslot], vpar, abort, limit) ||
-              !mbar_wait_bounded(&C->p_full[ob], ph, abort, limit) ||
-              !mbar_wait_bounded(&C->o_empty[ob], ph ^ 1u, abort, limit)) {
-            cache_error(p, abort, CERR_P);
-            break;
-          }
-          tc_fence_after();
-          const uint32_t va = kva + vslot * Sh::SLOT, pb = pa + ob * Sh::P;
-          // 32 tokens a step.  With D = 64 the upper half of M reads the next
-          // 8-token group (LBO = one atom): lanes 64-127 hold nothing of use.
-#pragma unroll
-          for (int term = 0; term < TERMS; ++term)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f8(tmem + (2 + ob) * N, sdesc(va + kk * 32 * D, ATOM, ATOM, SW),
-                     sdesc(pb + term * N * C_TILE + kk * 512, 128, 2048, 0), IDESC_O, (term | kk) != 0);
-          mma_commit(&C->empty[vslot]);
-          mma_commit(&C->o_full[ob]);
+        if (++slot == NS) {
+          slot = 0;
+          phase ^= 1u;
         }
-        vslot = next_v;
-        vpar = next_par;
+        next_v = slot;
+        next_vphase = phase;
+        if (++slot == NS) {
+          slot = 0;
+          phase ^= 1u;
+        }
       }
+      if (t > 0) {
+        const uint32_t ob = (t - 1) & 1, ph = static_cast<uint32_t>((t - 1) >> 1) & 1u;
+        if (!await(&C->full[vslot], vphase, CERR_FULL) || !await(&C->p_full[ob], ph, CERR_P)) break;
+        tc_fence_after();
+        const uint64_t v = vd + vslot * (Sh::SLOT >> 4), q = pd + ob * (Sh::P >> 4);
+        if (elect_one()) {
+          // 32 tokens a step
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_f8(tmem + (2 + ob) * N, v + kk * (2 * D), q + kk * 32, IDESC_O, kk != 0);
+          mma_commit(&C->o_full[ob]);
+          mma_commit(&C->empty[vslot]);
+        }
+      }
+      vslot = next_v;
+      vphase = next_vphase;
+    }
+    if (elect_one()) {
       mma_commit(&C->done);
       if (!mbar_wait_timed(&C->done, 0, limit)) cache_error(p, abort, CERR_DRAIN);
     }
@@ -580,12 +577,12 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
         // rows of D bytes, 16-byte chunks swizzled within 8-row atoms
         const int byte = lane * E;
         const int chunk = D == 128 ? (byte >> 4) ^ (r & 7) : (byte >> 4) ^ ((r >> 1) & 3);
-        uint8_t* dst = q_s + qb * Sh::Q + r * D + chunk * 16 + (byte & 15);
+        uint8_t* dst = q_s + qb * Sh::Q + r * D + chunk * 16 + (byte & 15);  // (R is a multiple of 8: all terms swizzle alike)
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
           const uint32_t c = e4m3x4(v[0], v[1], v[2], v[3]);
-          if constexpr (E == 4) *reinterpret_cast<uint32_t*>(dst + term * N * D) = c;
-          else *reinterpret_cast<uint16_t*>(dst + term * N * D) = static_cast<uint16_t>(c);
+          if constexpr (E == 4) *reinterpret_cast<uint32_t*>(dst + term * R * D) = c;
+          else *reinterpret_cast<uint16_t*>(dst + term * R * D) = static_cast<uint16_t>(c);
           take_off(v, c);
         }
         if (lane == 0) {
@@ -595,6 +592,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
           C->qs[qb][r] = amax <= 3.402823466e38f ? sc * p.scale_log2 : __int_as_float(0x7fc00000);
           C->pos[qb][r] = ps;
           C->low[qb][r] = p.window && p.window <= ps ? ps - p.window : -1;
+          C->out[qb][r] = (b * p.L + i) * p.H + h * p.G + g;
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read by the MMA
@@ -624,6 +622,18 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
       }
       return true;
     };
+    // the sum of a row's terms
+    auto load_terms = [&](uint32_t addr, float (&v)[HC]) {
+      float t[TERMS - 1][HC];
+      tmem_ld<HC>(addr, v);
+#pragma unroll
+      for (int i = 1; i < TERMS; ++i) tmem_ld<HC>(addr + i * R, t[i - 1]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 1; i < TERMS; ++i)
+#pragma unroll
+        for (int c = 0; c < HC; ++c) v[c] += t[i - 1][c];
+    };
     // joins tile j's O into the state
     auto join = [&](long long j, int qb, int tok0) -> bool {
       const uint32_t ob = j & 1, ph = static_cast<uint32_t>(j >> 1) & 1u;
@@ -634,11 +644,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
       }
       tc_fence_after();
       float o[HC];
-      tmem_ld<HC>(tmem + lanes + (2 + ob) * N + c0, o);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&C->o_empty[ob]);
+      load_terms(tmem + lanes + (2 + ob) * N + c0, o);
 #pragma unroll
       for (int c = 0; c < HC; ++c) {
         const float2 f = C->ab[ob][c0 + c];
@@ -692,11 +698,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
       }
       tc_fence_after();
       float s[HC];
-      tmem_ld<HC>(tmem + lanes + sb * N + c0, s);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&C->s_empty[sb]);
+      load_terms(tmem + lanes + sb * N + c0, s);
 #pragma unroll
       for (int c = 0; c < HC; ++c) s[c] *= C->qs[qb][c0 + c] * ks;
       if (flags & F_MASK) {
@@ -733,12 +735,11 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
 #pragma unroll
       for (int c = 0; c < HC; c += 4) {
         float v[4] = {pr[c], pr[c + 1], pr[c + 2], pr[c + 3]};
-        const int col = c0 + c;
-        uint8_t* dst = p_s + sb * Sh::P + (col >> 4) * 2048 + me * 16 + (col & 15);
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
+          const int col = term * R + c0 + c;
           const uint32_t q = e4m3x4(v[0], v[1], v[2], v[3]);
-          *reinterpret_cast<uint32_t*>(dst + term * N * C_TILE) = q;
+          *reinterpret_cast<uint32_t*>(p_s + sb * Sh::P + (col >> 4) * 2048 + me * 16 + (col & 15)) = q;
           if (term + 1 < TERMS) take_off(v, q);
         }
       }
@@ -754,32 +755,40 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
           if (lane == 0) cache_error(p, abort, CERR_FULL);
           break;
         }
-        // each half of the warps takes half of the row (no other thread touches it; order of chunks is of no matter)
+        // each half of the warps takes half of the row's chunks; the lanes begin
+        // at different ones, so that they meet no bank twice
+        constexpr int CH = D / 32;
         uint4* row = reinterpret_cast<uint4*>(kv_s + d.vslot * Sh::SLOT + me * D);
         uint32_t bits[2] = {0, 0};
         if (!any) {
+          // (pages that are not there arrived as zeros)
+          if ((d.pages >> page_of) & 1) {
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) row[half * (D / 32) + i] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < CH; ++i) row[half * CH + ((i + me) & (CH - 1))] = make_uint4(0, 0, 0, 0);
+          }
         } else if (!all) {
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
+          for (int i = 0; i < CH; ++i) {
             // chunk i of the row's half, wherever the swizzle put it
-            const int chunk = half * (D / 32) + i;
+            const int chunk = half * CH + i;
             const int at = D == 128 ? chunk ^ (me & 7) : chunk ^ ((me >> 1) & 3);
-            uint4 x = row[at];
-            uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            bool hit = false;
+            const uint4 x = row[at];
+            uint32_t w[4] = {x.x, x.y, x.z, x.w}, hit = 0;
+            // a code of ones but for its sign carries into the sign's place
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q) hit |= ((w[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+            if (hit) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (((w[q] >> (8 * e)) & 0x7Fu) == 0x7Fu) {
-                  const int bit = i * 16 + q * 4 + e;
-                  bits[bit >> 5] |= 1u << (bit & 31);
-                  w[q] &= ~(0xFFu << (8 * e));
-                  hit = true;
-                }
-            if (hit) row[at] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (((w[q] >> (8 * e)) & 0x7Fu) == 0x7Fu) {
+                    const int bit = i * 16 + q * 4 + e;
+                    bits[bit >> 5] |= 1u << (bit & 31);
+                    w[q] &= ~(0xFFu << (8 * e));
+                  }
+              row[at] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
         }
         if (p.L > 1) {
@@ -790,6 +799,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // P (and cleared values) are read by the MMA
+      tc_fence_before();                                             // S and the O before have been read
       __syncwarp();
       if (lane == 0) mbar_arrive(&C->p_full[sb]);
       if (!(flags & F_FIRST) && !join(t - 1, qb, prev_tok0)) break;
@@ -816,8 +826,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
           const float sum = (v.x + v.y) + (v.z + v.w);
           if (r < rows) {
             if (whole) {
-              const int row = row0 + r, i = row / p.G, g = row % p.G;
-              const size_t at = (static_cast<size_t>(b) * p.L + i) * p.H + h * p.G + g;
+              const size_t at = C->out[qb][r];
               const float o = acc[c] * (sum == 0.f ? 0.f : 1.f / sum);
               if (me < D) {
                 if constexpr (HALF) reinterpret_cast<__half*>(p.out)[at * D + me] = __float2half_rn(o);
@@ -953,8 +962,9 @@ si_status launch_cache_rows(CacheParams& p, const si_cache* c, int n_sm, const s
   const long long rows = static_cast<long long>(p.L) * p.G;
   if (rows <= 8) return launch_cache<D, 8, HALF>(p, c, n_sm, opt, stream);
   if (rows <= 16) return launch_cache<D, 16, HALF>(p, c, n_sm, opt, stream);
-  if (rows <= 32) return launch_cache<D, 32, HALF>(p, c, n_sm, opt, stream);
-  return launch_cache<D, 64, HALF>(p, c, n_sm, opt, stream);
+  // (three terms of 64 rows do not fit into tensor memory)
+  if (rows <= 32 || HALF) return launch_cache<D, 32, HALF>(p, c, n_sm, opt, stream);
+  return launch_cache<D, HALF ? 32 : 64, HALF>(p, c, n_sm, opt, stream);
 }
 
 }  // namespace
