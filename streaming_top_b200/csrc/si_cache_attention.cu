@@ -211,6 +211,7 @@ struct CacheCtrl {
   alignas(16) float red[2][R][4];     // per row and quadrant of lanes: the tile's maximum
   alignas(16) float sum[R][4];        // the same: the unit's sum
   alignas(16) float2 ab[2][R];        // per row: factors of the state and of the tile's O
+  alignas(16) float4 col[8][R / 2];   // per warp and row: score scale, the tile's maximum, factors of the state and of the tile
   uint32_t nan_bits[2][C_TILE][4];    // dims whose value is NaN, for tokens that only some rows see
   int nan_tile[2];
   long long scan[C_THREADS / 32];
@@ -606,7 +607,9 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const float ninf = -__int_as_float(0x7f800000);
     const int page_of = me / p.page;
-    float m[HC], l[HC], acc[HC];
+    float m = ninf;  // lane c: running maximum of row c0 + c
+    float l[HC], acc[HC];
+    float4* col = C->col[warp - 4];
     uint32_t n_unit = 0, n_x = 0;
     int prev_tok0 = 0;
 
@@ -682,9 +685,9 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
           if (lane == 0) cache_error(p, abort, CERR_Q);
           break;
         }
+        m = ninf;
 #pragma unroll
         for (int c = 0; c < HC; ++c) {
-          m[c] = ninf;
           l[c] = 0.f;
           acc[c] = 0.f;
         }
@@ -699,8 +702,9 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
       tc_fence_after();
       float s[HC];
       load_terms(tmem + lanes + sb * N + c0, s);
+      // (a row's own scale is positive: it can follow the maximum)
 #pragma unroll
-      for (int c = 0; c < HC; ++c) s[c] *= C->qs[qb][c0 + c] * ks;
+      for (int c = 0; c < HC; ++c) s[c] *= ks;
       if (flags & F_MASK) {
         const int tok = tok0 + me;
         const bool there = (d.pages >> page_of) & 1;
@@ -716,31 +720,41 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
         if (lane == 0) C->red[sb][c0 + c][quad] = w;
       }
       if (!meet()) break;
-      float pr[HC];
-#pragma unroll
-      for (int c = 0; c < HC; ++c) {
-        const float4 r = *reinterpret_cast<const float4*>(C->red[sb][c0 + c]);
-        const float mt = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w));
-        const float e = ex2(s[c] - (mt == ninf ? 0.f : mt));
-        // the state's factor and the tile's: one of them is 1
-        const float f = mt == m[c] ? 1.f : ex2(-fabsf(m[c] - mt));
-        const bool up = mt > m[c];
+      // a lane a row: the tile's maximum, the state's factor and the tile's (one of them is 1)
+      if (lane < HC) {
+        const float4 r = *reinterpret_cast<const float4*>(C->red[sb][c0 + lane]);
+        const float q = C->qs[qb][c0 + lane], mt = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)) * q;
+        const float f = mt == m ? 1.f : ex2(-fabsf(m - mt));
+        const bool up = mt > m;
         const float fa = up ? f : 1.f, fb = up ? 1.f : f;
-        m[c] = fmaxf(m[c], mt);
-        l[c] = fmaf(e, fb, l[c] * fa);
-        pr[c] = e * rv;
-        if (lane == 0 && quad == 0) C->ab[sb][c0 + c] = make_float2(fa, fb * vref * (1.f / 256.f));
+        m = fmaxf(m, mt);
+        col[lane] = make_float4(q, mt == ninf ? 0.f : mt, fa, fb);
+        if (quad == 0) C->ab[sb][c0 + lane] = make_float2(fa, fb * vref * (1.f / 256.f));
       }
-      // P's terms, the row of a token contiguous along N in groups of 16
+      __syncwarp();
+      // P in half precision (11 bits), then its terms, the row of a token
+      // contiguous along N in groups of 16
 #pragma unroll
       for (int c = 0; c < HC; c += 4) {
-        float v[4] = {pr[c], pr[c + 1], pr[c + 2], pr[c + 3]};
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 k = col[c + i];
+          const float e = ex2(fmaf(s[c + i], k.x, -k.y));
+          l[c + i] = fmaf(e, k.w, l[c + i] * k.z);
+          v[i] = e * rv;
+        }
+        __half2 x = __floats2half2_rn(v[0], v[1]), y = __floats2half2_rn(v[2], v[3]);
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
-          const int col = term * R + c0 + c;
-          const uint32_t q = e4m3x4(v[0], v[1], v[2], v[3]);
-          *reinterpret_cast<uint32_t*>(p_s + sb * Sh::P + (col >> 4) * 2048 + me * 16 + (col & 15)) = q;
-          if (term + 1 < TERMS) take_off(v, q);
+          const uint32_t qx = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t qy = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(y), __NV_SATFINITE, __NV_E4M3);
+          const int at = term * R + c0 + c;
+          *reinterpret_cast<uint32_t*>(p_s + sb * Sh::P + (at >> 4) * 2048 + me * 16 + (at & 15)) = qx | (qy << 16);
+          if (term + 1 < TERMS) {
+            x = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(qx), __NV_E4M3)));
+            y = __hsub2(y, __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(qy), __NV_E4M3)));
+          }
         }
       }
       if (flags & F_MASK) {
@@ -822,24 +836,28 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
 #pragma unroll
         for (int c = 0; c < HC; ++c) {
           const int r = c0 + c;
+          if (r < rows && me < D) {
+            const float4 v = *reinterpret_cast<const float4*>(C->sum[r]);
+            const float sum = (v.x + v.y) + (v.z + v.w);
+            if (whole) {
+              const size_t at = static_cast<size_t>(C->out[qb][r]) * D + me;
+              const float o = acc[c] * (sum == 0.f ? 0.f : 1.f / sum);
+              if constexpr (HALF) reinterpret_cast<__half*>(p.out)[at] = __float2half_rn(o);
+              else reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o);
+            } else {
+              part[r * D + me] = acc[c];
+            }
+          }
+        }
+        if (quad == 0 && lane < HC && c0 + lane < rows) {
+          const int r = c0 + lane;
           const float4 v = *reinterpret_cast<const float4*>(C->sum[r]);
           const float sum = (v.x + v.y) + (v.z + v.w);
-          if (r < rows) {
-            if (whole) {
-              const size_t at = C->out[qb][r];
-              const float o = acc[c] * (sum == 0.f ? 0.f : 1.f / sum);
-              if (me < D) {
-                if constexpr (HALF) reinterpret_cast<__half*>(p.out)[at * D + me] = __float2half_rn(o);
-                else reinterpret_cast<__nv_bfloat16*>(p.out)[at * D + me] = __float2bfloat16_rn(o);
-              }
-              if (me == 0 && p.lse) p.lse[at] = sum == 0.f ? ninf : (m[c] + log2f(sum)) * LN2;
-            } else {
-              if (me < D) part[r * D + me] = acc[c];
-              if (me == 0) {
-                part[R * D + r] = m[c];
-                part[R * D + R + r] = sum;
-              }
-            }
+          if (!whole) {
+            part[R * D + r] = m;
+            part[R * D + R + r] = sum;
+          } else if (p.lse) {
+            p.lse[C->out[qb][r]] = sum == 0.f ? ninf : (m + log2f(sum)) * LN2;
           }
         }
         if (begins && !whole && me == 0 && half == 0) {
