@@ -81,19 +81,21 @@ struct CacheParams {
 
 // A tile, as the scheduler publishes it.
 struct TileDesc {
-  int flags, tok0, b, h, row0, rows, vslot, vparity;
+  int flags, b, h, row0, rows, vslot, vparity;
   int p_lo, p_hi;       // positions of the sequence's first and last query
   int pages;            // bit j: page j of the tile is there
   int seg;              // 0: the CTA's first segment of a unit, 1: a later one (its slot)
   int left;             // the unit's tiles behind this one
   float vref;
-  float ks[8], rv[8];   // a page's key scale, and value scale / v_ref * 256
+  int tok[8];           // a page's first token
+  float ks[8], rv[8];   // its key scale, and value scale / v_ref * 256
 };
 
-// The visible tiles of a sequence: n_sink_tiles from 0 on, then those from `first` on.
+// The visible pages of a sequence: sink_pages from 0 on, then those from `first`
+// on.  Its tiles take them in this order, 128 tokens' worth each, so that the
+// sinks share a tile with the window.
 struct Span {
-  int first, sink_tiles, tiles;
-  long long lo, hi, sink;  // visible tokens: [0, sink) and [lo, hi)
+  int first, sink_pages, pages, tiles;
   int p_lo, p_hi;
 };
 
@@ -101,13 +103,14 @@ __device__ __forceinline__ Span span_of(const CacheParams& p, int b) {
   Span s;
   const long long len = p.lens[b], cap = static_cast<long long>(p.max_pages) * p.page;
   const long long p_lo = len - p.L, p_hi = len - 1;
-  s.hi = max(min(p_hi + 1, cap), 0ll);
-  s.lo = p.window ? min(max(p_lo - p.window + 1, 0ll), s.hi) : 0;
-  s.sink = p.window ? min(static_cast<long long>(p.n_sink), s.hi) : 0;
-  s.first = static_cast<int>(s.lo / C_TILE);
-  const int main_tiles = static_cast<int>((s.hi + C_TILE - 1) / C_TILE) - s.first;
-  s.sink_tiles = min(static_cast<int>((s.sink + C_TILE - 1) / C_TILE), s.first);
-  s.tiles = max(main_tiles + s.sink_tiles, 1);  // an empty unit still writes its rows
+  // visible tokens: [0, sink) and [lo, hi)
+  const long long hi = max(min(p_hi + 1, cap), 0ll);
+  const long long lo = p.window ? min(max(p_lo - p.window + 1, 0ll), hi) : 0;
+  const long long sink = p.window ? min(static_cast<long long>(p.n_sink), hi) : 0;
+  s.first = static_cast<int>(lo / p.page);
+  s.sink_pages = min(static_cast<int>((sink + p.page - 1) / p.page), s.first);
+  s.pages = static_cast<int>((hi + p.page - 1) / p.page) - s.first + s.sink_pages;
+  s.tiles = max((s.pages * p.page + C_TILE - 1) / C_TILE, 1);  // an empty unit still writes its rows
   s.p_lo = static_cast<int>(max(p_lo, -(1ll << 30)));
   s.p_hi = static_cast<int>(p_hi < 0 ? -1 : p_hi);
   return s;
@@ -191,7 +194,7 @@ struct CacheShape {
   static constexpr int SLOT = C_TILE * D;      // a K or V tile
   static constexpr int Q = N * D;              // one q buffer
   static constexpr int P = N * C_TILE;         // one P buffer
-  static constexpr int SLOTS = CTAS == 2 ? (D == 128 ? 5 : 10) : (R == 32 || D == 64 ? 10 : 8);
+  static constexpr int SLOTS = CTAS == 2 ? (D == 128 ? (R == 16 && HALF ? 4 : 5) : 10) : (R == 32 || D == 64 ? 10 : 8);
   static constexpr int TMEM = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 4 * N <= 256 ? 256 : 512;  // S and O, two buffers each
   static_assert(4 * N <= 512 / CTAS, "tensor memory");
 };
@@ -213,7 +216,7 @@ struct CacheCtrl {
   alignas(16) float2 ab[2][R];        // per row: factors of the state and of the tile's O
   alignas(16) float4 col[8][R / 2];   // per warp and row: score scale, the tile's maximum, factors of the state and of the tile
   uint32_t nan_bits[2][C_TILE][4];    // dims whose value is NaN, for tokens that only some rows see
-  int nan_tile[2];
+  int nan_tok[2][8], nan_tile[2];     // first tokens of such a tile's pages, and its number
   long long scan[C_THREADS / 32];
   long long total, start, stop;       // tiles of the batch; this CTA's run
   int b0;                             // the sequence in which the run starts,
@@ -363,17 +366,22 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
       const int h = hn / p.chunks, row0 = (hn % p.chunks) * R;
       const int cnt = static_cast<int>(min(static_cast<long long>(min(group, sp.tiles - k)), n_tiles - t));
       const int kk = k + gi;
-      const int tile = kk < sp.sink_tiles ? kk : sp.first + kk - sp.sink_tiles;
-      const long long tok = static_cast<long long>(tile) * C_TILE + pj * p.page;
-      bool there = gi < cnt && tok < sp.hi && (tok + p.page > sp.lo || tok < sp.sink);
+      const int nth = kk * npg + pj;  // of the sequence's visible pages
+      const int pg = nth < sp.sink_pages ? nth : sp.first + nth - sp.sink_pages;
+      const int tok = pg * p.page;
+      bool there = gi < cnt && nth < sp.pages;
       int id = -1;
-      if (there) id = p.table[static_cast<size_t>(b) * p.max_pages + tok / p.page];
+      if (there) id = p.table[static_cast<size_t>(b) * p.max_pages + pg];
       there = there && id >= 0 && id < p.n_pages;
       const size_t ph = static_cast<size_t>(there ? id : 0) * p.H_kv + h;
       const float ks = there ? p.ks[ph] : 0.f, vs = there ? p.vs[ph] : 0.f;
       // coordinates past the pool read zeros
       const int y = there ? static_cast<int>(ph * p.page) : static_cast<int>(p.rows_total);
       const uint32_t there_bits = __ballot_sync(0xFFFFFFFFu, there);
+      // pages that every row sees whole
+      const uint32_t clear_bits = __ballot_sync(
+          0xFFFFFFFFu, tok + p.page - 1 <= sp.p_lo && (!p.window || tok > static_cast<long long>(sp.p_hi) - p.window ||
+                                                       static_cast<long long>(tok) + p.page <= p.n_sink));
       float vref = vs;
       for (int o = npg >> 1; o; o >>= 1) vref = fmaxf(vref, __shfl_xor_sync(0xFFFFFFFFu, vref, o));
       const float rv = vref > 0.f ? vs / vref * 256.f : 0.f;
@@ -391,16 +399,14 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
           vphase ^= 1u;
         }
         if (gi == i) {
+          d.tok[pj] = tok;
           d.ks[pj] = ks;
           d.rv[pj] = rv;
           if (pj == 0) {
-            const long long tok0 = static_cast<long long>(tile) * C_TILE;
-            const uint32_t pages = (there_bits >> (gi * npg)) & (npg == 32 ? ~0u : (1u << npg) - 1u);
-            const bool all = pages == (1u << npg) - 1u && tok0 + C_TILE - 1 <= sp.p_lo &&
-                             (!p.window || tok0 > static_cast<long long>(sp.p_hi) - p.window || tok0 + C_TILE <= p.n_sink);
+            const uint32_t pages = (there_bits >> (gi * npg)) & ((1u << npg) - 1u);
+            const bool every = pages == (1u << npg) - 1u && ((clear_bits >> (gi * npg)) & ((1u << npg) - 1u)) == (1u << npg) - 1u;
             const bool first = t == 0 || kk == 0, last = t == n_tiles - 1 || kk == sp.tiles - 1;
-            d.flags = (first ? F_FIRST : 0) | (last ? F_LAST : 0) | (all ? 0 : F_MASK);
-            d.tok0 = static_cast<int>(tok0);
+            d.flags = (first ? F_FIRST : 0) | (last ? F_LAST : 0) | (every ? 0 : F_MASK);
             d.b = b;
             d.h = h;
             d.row0 = row0;
@@ -611,7 +617,6 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
     float l[HC], acc[HC];
     float4* col = C->col[warp - 4];
     uint32_t n_unit = 0, n_x = 0;
-    int prev_tok0 = 0;
 
     // all eight warps meet (bounded)
     auto meet = [&]() -> bool {
@@ -638,7 +643,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
         for (int c = 0; c < HC; ++c) v[c] += t[i - 1][c];
     };
     // joins tile j's O into the state
-    auto join = [&](long long j, int qb, int tok0) -> bool {
+    auto join = [&](long long j, int qb) -> bool {
       const uint32_t ob = j & 1, ph = static_cast<uint32_t>(j >> 1) & 1u;
       const bool got = mbar_wait_bounded(&C->o_full[ob], ph, abort, limit);
       if (!__all_sync(0xFFFFFFFFu, got)) {
@@ -658,7 +663,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
 #pragma unroll 1
         for (int k = 0; k < C_TILE; ++k)
           if ((C->nan_bits[ob][k][me >> 5] >> (me & 31)) & 1u) {
-            const int tok = tok0 + k;
+            const int tok = C->nan_tok[ob][k / p.page] + k % p.page;
 #pragma unroll
             for (int c = 0; c < HC; ++c)
               if (tok <= C->pos[qb][c0 + c] && (tok > C->low[qb][c0 + c] || tok < p.n_sink))
@@ -676,7 +681,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
         break;
       }
       const TileDesc& d = C->desc[ds];
-      const int flags = d.flags, tok0 = d.tok0;
+      const int flags = d.flags, tok = d.tok[page_of] + me % p.page;
       const float ks = d.ks[page_of], rv = d.rv[page_of], vref = d.vref;
       if (flags & F_FIRST) {
         ++n_unit;
@@ -706,7 +711,6 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
 #pragma unroll
       for (int c = 0; c < HC; ++c) s[c] *= ks;
       if (flags & F_MASK) {
-        const int tok = tok0 + me;
         const bool there = (d.pages >> page_of) & 1;
 #pragma unroll
         for (int c = 0; c < HC; ++c) {
@@ -761,7 +765,6 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
         // Values of tokens that no row sees may hold anything; 0 * NaN would
         // reach the sums.  They are cleared; of tokens that some rows see, NaN
         // codes are cleared and noted.
-        const long long tok = static_cast<long long>(tok0) + me;
         const bool any = tok <= d.p_hi && (!p.window || tok > static_cast<long long>(d.p_lo) - p.window || tok < p.n_sink);
         const bool all = tok <= d.p_lo && (!p.window || tok > static_cast<long long>(d.p_hi) - p.window || tok < p.n_sink);
         got = mbar_wait_bounded(&C->full[d.vslot], d.vparity, abort, limit);
@@ -809,6 +812,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
           // bits of dims [half * D / 2, ...): two words with D = 128, one with D = 64
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) C->nan_bits[sb][me][half * (D / 64) + i] = bits[i];
+          if (me % p.page == 0) C->nan_tok[sb][page_of] = tok;
           if (bits[0] | bits[1]) C->nan_tile[sb] = static_cast<int>(t);
         }
       }
@@ -816,12 +820,11 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
       tc_fence_before();                                             // S and the O before have been read
       __syncwarp();
       if (lane == 0) mbar_arrive(&C->p_full[sb]);
-      if (!(flags & F_FIRST) && !join(t - 1, qb, prev_tok0)) break;
-      prev_tok0 = tok0;
+      if (!(flags & F_FIRST) && !join(t - 1, qb)) break;
       if (flags & F_LAST) {
         // the sums over the tokens, then the unit's rows or a partial result
         if (!meet()) break;  // ab of this tile is visible
-        if (!join(t, qb, tok0)) break;
+        if (!join(t, qb)) break;
 #pragma unroll
         for (int c = 0; c < HC; ++c) {
           float v = l[c];
@@ -940,11 +943,11 @@ si_status launch_cache(CacheParams& p, const si_cache* c, int n_sm, const si_opt
   if (st != SI_OK) return st;
   p.chunks = (p.L * p.G + R - 1) / R;
   // the tiles that a sequence can have at most
-  const long long cap = (static_cast<long long>(p.max_pages) * p.page + C_TILE - 1) / C_TILE;
-  long long tiles = cap;
+  long long pages = p.max_pages;
   if (p.window)
-    tiles = std::min(cap, (static_cast<long long>(p.window) + p.L + C_TILE - 2) / C_TILE + 1 +
-                              (static_cast<long long>(p.n_sink) + C_TILE - 1) / C_TILE);
+    pages = std::min(pages, (static_cast<long long>(p.window) + p.L - 2) / p.page + 2 +
+                                (static_cast<long long>(p.n_sink) + p.page - 1) / p.page);
+  const long long tiles = (pages * p.page + C_TILE - 1) / C_TILE;
   p.cut = tiles > C_WHOLE;
   const long long units = static_cast<long long>(p.B) * p.H_kv * p.chunks;
   const long long most = std::min(n_sm * Sh::CTAS, C_MAX_CTAS);
