@@ -292,11 +292,15 @@ _FLOAT_DTYPES = {torch.bfloat16: SI_DTYPE_BF16, torch.float16: SI_DTYPE_FP16}
 
 
 def _need(name, t, dtype, device, shape=None):
-    """A contiguous CUDA tensor of the dtype, on the device (and of the shape)."""
-    if t.dtype != dtype or t.device != device or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device if device.type == 'cuda' else 'CUDA'}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have the shape {shape} (got {tuple(t.shape)})")
+    """A contiguous CUDA tensor of the dtype, on the device of that index (and
+    of the shape).  Every call makes several of these checks, and a small
+    call's time is the host's: one expression where nothing is wrong."""
+    if (t.dtype is dtype and t.get_device() == device and device >= 0 and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
+    if t.dtype is not dtype or t.get_device() != device or device < 0 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on " + (f"cuda:{device}" if device >= 0 else "a GPU"))
+    raise ValueError(f"{name} must have the shape {tuple(shape)} (got {tuple(t.shape)})")
 
 
 def _float_dtype(name, t):
@@ -307,15 +311,14 @@ def _float_dtype(name, t):
 
 
 def _enqueue(where, device, stream, call):
-    """call(stream pointer) on `stream`, or on the current stream of `device`,
-    with that device current for the launches."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if torch.cuda.current_device() == device.index:
-        st = call(stream.cuda_stream)
+    """call(stream pointer) on `stream`, or on the current stream of the
+    device, with that device current for the launches."""
+    ptr = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        st = call(ptr)
     else:
         with torch.cuda.device(device):
-            st = call(stream.cuda_stream)
+            st = call(ptr)
     if st != SI_OK:
         raise SIError(st, where)
 
@@ -330,14 +333,14 @@ class PagedCache:
     def __init__(self, k_pages, v_pages, k_scale, v_scale):
         if k_pages.dim() != 4 or k_pages.dtype not in (torch.float8_e4m3fn, torch.uint8):
             raise ValueError("k_pages [n_pages, H_kv, page, D] must hold e4m3 codes (float8_e4m3fn or uint8)")
-        device = k_pages.device
+        device, shape = k_pages.get_device(), k_pages.shape
         _need("k_pages", k_pages, k_pages.dtype, device)
-        _need("v_pages", v_pages, k_pages.dtype, device, tuple(k_pages.shape))
-        _need("k_scale", k_scale, torch.float32, device, tuple(k_pages.shape[:2]))
-        _need("v_scale", v_scale, torch.float32, device, tuple(k_pages.shape[:2]))
+        _need("v_pages", v_pages, k_pages.dtype, device, shape)
+        _need("k_scale", k_scale, torch.float32, device, shape[:2])
+        _need("v_scale", v_scale, torch.float32, device, shape[:2])
         self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
-        self.device = device
-        self.n_pages, self.kv_heads, self.page, self.dim = k_pages.shape
+        self.device = device  # index
+        self.n_pages, self.kv_heads, self.page, self.dim = shape
         self._c = _Cache(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                          self.n_pages, self.kv_heads, self.page, self.dim)
 
@@ -364,15 +367,15 @@ def cache_append(cache: PagedCache, k, v, table, lens, *, n_new=None, stream=Non
         n_new.data_ptr() if n_new is not None else None, B, L, table.shape[1], dt, s))
 
 
-def _attention_outputs(q, out, lse):
+def _attention_outputs(q, device, out, lse):
     if out is None:
         out = torch.empty_like(q)
     else:
-        _need("out", out, q.dtype, q.device, tuple(q.shape))
+        _need("out", out, q.dtype, device, q.shape)
     if lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        lse = q.new_empty(q.shape[:3], dtype=torch.float32)
     else:
-        _need("lse", lse, torch.float32, q.device, tuple(q.shape[:3]))
+        _need("lse", lse, torch.float32, device, q.shape[:3])
     return out, lse
 
 
@@ -381,8 +384,8 @@ def _attention_options(device, workspace, device_status):
         return None
     o = Options()
     if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
         o.workspace = workspace.data_ptr()
         o.workspace_bytes = workspace.numel() * workspace.element_size()
     if device_status is not None:
@@ -412,7 +415,7 @@ def cache_attention(q, cache: PagedCache, table, lens, *, window: int = 0, n_sin
     _need("q", q, q.dtype, device)
     _need("table", table, torch.int32, device, (B, table.shape[1]))
     _need("lens", lens, torch.int32, device, (B,))
-    out, lse = _attention_outputs(q, out, lse)
+    out, lse = _attention_outputs(q, device, out, lse)
     o = _attention_options(device, workspace, device_status)
     _enqueue("si_cache_attention", device, stream, lambda s: _lib.si_cache_attention(
         q.data_ptr(), cache._c, table.data_ptr(), lens.data_ptr(), B, L, H, table.shape[1], window, n_sink, scale,
@@ -435,14 +438,14 @@ def window_attention(q, k, v, *, window: int, n_sink: int = 0, lens=None, scale:
         raise ValueError("q [B, S, H, D] and k, v [B, S, H_kv, D] expected")
     B, S, H, D = q.shape
     dt = _float_dtype("q", q)
-    device = q.device
+    device = q.get_device()
     _need("q", q, q.dtype, device)
     shape = (B, S, k.shape[2], D)
     _need("k", k, q.dtype, device, shape)
     _need("v", v, q.dtype, device, shape)
     if lens is not None:
         _need("lens", lens, torch.int32, device, (B,))
-    out, lse = _attention_outputs(q, out, lse)
+    out, lse = _attention_outputs(q, device, out, lse)
     o = _attention_options(device, None, device_status)
     _enqueue("si_window_attention", device, stream, lambda s: _lib.si_window_attention(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr() if lens is not None else None, B, S, H,
@@ -468,7 +471,7 @@ def cache_reserve(cache: PagedCache, table, lens, refs, n_new, *, status=None, s
     n_seq, max_pages = _sequence_state(cache, table, lens, refs)
     _need("n_new", n_new, torch.int32, cache.device, (n_seq,))
     if status is None:
-        status = torch.empty((n_seq,), dtype=torch.int32, device=cache.device)
+        status = table.new_empty((n_seq,))
     else:
         _need("status", status, torch.int32, cache.device, (n_seq,))
     _enqueue("si_cache_reserve", cache.device, stream, lambda s: _lib.si_cache_reserve(
@@ -487,7 +490,7 @@ def cache_fork(cache: PagedCache, table, lens, refs, src, dst, *, share: bool = 
     _need("src", src, torch.int32, cache.device, (n,))
     _need("dst", dst, torch.int32, cache.device, (n,))
     if status is None:
-        status = torch.empty((n,), dtype=torch.int32, device=cache.device)
+        status = table.new_empty((n,))
     else:
         _need("status", status, torch.int32, cache.device, (n,))
     _enqueue("si_cache_fork", cache.device, stream, lambda s: _lib.si_cache_fork(
@@ -511,11 +514,11 @@ def cache_compact(cache: PagedCache, table, refs, *, used=None, moved=None, stre
     [n_pages] int32, each used page's new place, -1 for the others)."""
     n_seq, max_pages = _sequence_state(cache, table, None, refs)
     if used is None:
-        used = torch.empty((1,), dtype=torch.int32, device=cache.device)
+        used = table.new_empty((1,))
     else:
         _need("used", used, torch.int32, cache.device, (1,))
     if moved is None:
-        moved = torch.empty((cache.n_pages,), dtype=torch.int32, device=cache.device)
+        moved = table.new_empty((cache.n_pages,))
     else:
         _need("moved", moved, torch.int32, cache.device, (cache.n_pages,))
     _enqueue("si_cache_compact", cache.device, stream, lambda s: _lib.si_cache_compact(
