@@ -65,7 +65,7 @@ __device__ __forceinline__ float2 decode2(uint32_t codes) {
 constexpr int AP_VECS = 8;
 
 template <int D, bool HALF>
-__global__ void cache_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(256, 4) cache_append_kernel(const AppendParams p) {
   constexpr int VROW = D / 8;  // 16-byte input vectors of a row
   __shared__ uint32_t s_amax[8];
   long long u = blockIdx.x;

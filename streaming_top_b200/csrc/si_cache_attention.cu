@@ -31,8 +31,9 @@
 //
 // Warps: 0 schedules (walks the tiles, reads page table and scales ahead,
 // publishes tile descriptors) and loads pages by TMA; 1 issues the MMAs; 2-3
-// split the queries into terms; 4-11 do the softmax: the two warpgroups take
-// half of the rows each, a thread one token (and later one dim).
+// split the queries into terms; the rest do the softmax: two or four
+// warpgroups take a share of the rows each, a thread one token (and later one
+// dim).
 // Every wait is bounded; on expiry SI_ERR_TIMEOUT is recorded, copies and MMAs
 // in flight are drained and the kernel exits.
 #include <cuda.h>
@@ -51,7 +52,6 @@
 namespace si {
 namespace {
 
-constexpr int C_THREADS = 384;
 constexpr int C_TILE = 128;      // tokens of a tile
 constexpr int C_ND = 8;          // tile descriptors in flight
 constexpr int C_WHOLE = 4;       // units of at most this many tiles are not cut
@@ -191,6 +191,12 @@ struct CacheShape {
   static constexpr int TERMS = HALF ? 3 : 2;   // e4m3 terms of q and of P
   static constexpr int N = (TERMS * R + 15) / 16 * 16;  // the MMAs' N: term i of row r is column i R + r
   static constexpr int CTAS = R <= 16 ? 2 : 1; // per SM
+  // Softmax warpgroups, each with a share of the rows.  Eight rows a thread at
+  // most (sixteen of 64): with 32 the unrolled loop no longer fits the
+  // instruction cache, and 2 warpgroups wait more than they issue.
+  static constexpr int WG = R >= 32 ? 4 : 2;
+  static constexpr int HC = R / WG;            // rows of a thread
+  static constexpr int THREADS = 128 + 128 * WG;
   static constexpr int SLOT = C_TILE * D;      // a K or V tile
   static constexpr int Q = N * D;              // one q buffer
   static constexpr int P = N * C_TILE;         // one P buffer
@@ -214,10 +220,10 @@ struct CacheCtrl {
   alignas(16) float red[2][R][4];     // per row and quadrant of lanes: the tile's maximum
   alignas(16) float sum[R][4];        // the same: the unit's sum
   alignas(16) float2 ab[2][R];        // per row: factors of the state and of the tile's O
-  alignas(16) float4 col[8][R / 2];   // per warp and row: score scale, the tile's maximum, factors of the state and of the tile
-  uint32_t nan_bits[2][C_TILE][4];    // dims whose value is NaN, for tokens that only some rows see
+  alignas(16) float4 col[4 * Sh::WG][Sh::HC];   // per warp and row: score scale, the tile's maximum, factors of the state and of the tile
+  uint16_t nan_bits[2][C_TILE][D / 16];  // dims whose value is NaN, for tokens that only some rows see
   int nan_tok[2][8], nan_tile[2];     // first tokens of such a tile's pages, and its number
-  long long scan[C_THREADS / 32];
+  long long scan[Sh::THREADS / 32];
   long long total, start, stop;       // tiles of the batch; this CTA's run
   int b0;                             // the sequence in which the run starts,
   long long before0;                  // and the tiles of one (head, chunk) in the sequences before it
@@ -226,11 +232,11 @@ struct CacheCtrl {
 };
 
 template <int D, int R, bool HALF>
-__global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
+__global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape<D, R, HALF>::CTAS))
     cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                            const CacheParams p) {
   using Sh = CacheShape<D, R, HALF>;
-  constexpr int N = Sh::N, TERMS = Sh::TERMS, NS = Sh::SLOTS, HC = R / 2;
+  constexpr int N = Sh::N, TERMS = Sh::TERMS, NS = Sh::SLOTS, HC = Sh::HC, WG = Sh::WG, C_THREADS = Sh::THREADS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* kv_s = smem;
@@ -248,17 +254,17 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
     }
     for (int s = 0; s < C_ND; ++s) {
       mbar_init(&C->d_full[s], 1);
-      mbar_init(&C->d_empty[s], 10);  // two q warps, eight softmax warps
+      mbar_init(&C->d_empty[s], 2 + 4 * WG);  // two q warps, the softmax warps
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&C->q_full[s], 2);
-      mbar_init(&C->q_empty[s], 9);   // the MMAs' commit, eight softmax warps
+      mbar_init(&C->q_empty[s], 1 + 4 * WG);  // the MMAs' commit, the softmax warps
       mbar_init(&C->s_full[s], 1);
-      mbar_init(&C->p_full[s], 8);
+      mbar_init(&C->p_full[s], 4 * WG);
       mbar_init(&C->o_full[s], 1);
       C->nan_tile[s] = -1;
     }
-    mbar_init(&C->xbar, 8);
+    mbar_init(&C->xbar, 4 * WG);
     mbar_init(&C->done, 1);
     *abort = 0;
     if (p.cut) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -551,27 +557,31 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
       ++n_unit;
       const long long len = p.lens[b];
       constexpr int E = D / 32;  // dims of a lane
-#pragma unroll 4
-      for (int r = warp - 2; r < rows; r += 2) {
+      constexpr int BATCH = R / 2 < 8 ? R / 2 : 8;  // rows whose loads are under way together
+#pragma unroll 1
+      for (int r0 = warp - 2; r0 < rows; r0 += 2 * BATCH) {
+        uint32_t raw[BATCH][E / 2];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+          const int row = row0 + min(r0 + 2 * j, rows - 1), i = row / p.G, g = row % p.G;
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(
+              p.q + ((((static_cast<size_t>(b) * p.L + i) * p.H) + h * p.G + g) * D + lane * E) * 2);
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) raw[j][e] = src[e];
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+        const int r = r0 + 2 * j;
+        if (r >= rows) break;
         const int row = row0 + r, i = row / p.G, g = row % p.G;
-        const size_t at = (((static_cast<size_t>(b) * p.L + i) * p.H) + h * p.G + g) * D + lane * E;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (HALF) {
-          const __half2* s = reinterpret_cast<const __half2*>(p.q + at * 2);
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e) {
-            const float2 f = __half22float2(s[e]);
-            v[2 * e] = f.x;
-            v[2 * e + 1] = f.y;
-          }
-        } else {
-          const __nv_bfloat162* s = reinterpret_cast<const __nv_bfloat162*>(p.q + at * 2);
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) {
-            const float2 f = __bfloat1622float2(s[e]);
-            v[2 * e] = f.x;
-            v[2 * e + 1] = f.y;
-          }
+        for (int e = 0; e < E / 2; ++e) {
+          float2 f;
+          if constexpr (HALF) f = __half22float2(*reinterpret_cast<const __half2*>(&raw[j][e]));
+          else f = make_float2(__uint_as_float(raw[j][e] << 16), __uint_as_float(raw[j][e] & 0xFFFF0000u));
+          v[2 * e] = f.x;
+          v[2 * e + 1] = f.y;
         }
         const float amax = warp_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
         // 2^x, so that amax / 2^x is in [224, 448]: the exponent as it stands in a float
@@ -601,6 +611,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
           C->low[qb][r] = p.window && p.window <= ps ? ps - p.window : -1;
           C->out[qb][r] = (b * p.L + i) * p.H + h * p.G + g;
         }
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read by the MMA
       __syncwarp();
@@ -608,7 +619,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int half = (warp - 4) >> 2, quad = warp & 3, c0 = half * HC;
+    const int part = (warp - 4) >> 2, quad = warp & 3, c0 = part * HC;  // its rows, and its share of a value row
     const int me = quad * 32 + lane;  // the token of a tile, and the dim of O
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const float ninf = -__int_as_float(0x7f800000);
@@ -618,7 +629,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
     float4* col = C->col[warp - 4];
     uint32_t n_unit = 0, n_x = 0;
 
-    // all eight warps meet (bounded)
+    // the softmax warps meet (bounded)
     auto meet = [&]() -> bool {
       __syncwarp();
       if (lane == 0) mbar_arrive(&C->xbar);
@@ -662,7 +673,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
         // a value that is NaN reaches the rows that see its token, in its dim
 #pragma unroll 1
         for (int k = 0; k < C_TILE; ++k)
-          if ((C->nan_bits[ob][k][me >> 5] >> (me & 31)) & 1u) {
+          if ((C->nan_bits[ob][k][me >> 4] >> (me & 15)) & 1u) {
             const int tok = C->nan_tok[ob][k / p.page] + k % p.page;
 #pragma unroll
             for (int c = 0; c < HC; ++c)
@@ -772,25 +783,25 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
           if (lane == 0) cache_error(p, abort, CERR_FULL);
           break;
         }
-        // each half of the warps takes half of the row's chunks; the lanes begin
-        // at different ones, so that they meet no bank twice
-        constexpr int CH = D / 32;
+        // each warpgroup takes a share of the row's chunks; the lanes begin at
+        // different ones, so that they meet no bank twice
+        constexpr int CH = D / 16 / WG;
         uint4* row = reinterpret_cast<uint4*>(kv_s + d.vslot * Sh::SLOT + me * D);
-        uint32_t bits[2] = {0, 0};
+        uint32_t found = 0;
         if (!any) {
           // (pages that are not there arrived as zeros)
           if ((d.pages >> page_of) & 1) {
 #pragma unroll
-            for (int i = 0; i < CH; ++i) row[half * CH + ((i + me) & (CH - 1))] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < CH; ++i) row[part * CH + ((i + me) & (CH - 1))] = make_uint4(0, 0, 0, 0);
           }
         } else if (!all) {
 #pragma unroll
           for (int i = 0; i < CH; ++i) {
-            // chunk i of the row's half, wherever the swizzle put it
-            const int chunk = half * CH + i;
+            // chunk i of the share, wherever the swizzle put it
+            const int chunk = part * CH + i;
             const int at = D == 128 ? chunk ^ (me & 7) : chunk ^ ((me >> 1) & 3);
             const uint4 x = row[at];
-            uint32_t w[4] = {x.x, x.y, x.z, x.w}, hit = 0;
+            uint32_t w[4] = {x.x, x.y, x.z, x.w}, hit = 0, bits = 0;
             // a code of ones but for its sign carries into the sign's place
 #pragma unroll
             for (int q = 0; q < 4; ++q) hit |= ((w[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
@@ -800,20 +811,22 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   if (((w[q] >> (8 * e)) & 0x7Fu) == 0x7Fu) {
-                    const int bit = i * 16 + q * 4 + e;
-                    bits[bit >> 5] |= 1u << (bit & 31);
+                    bits |= 1u << (q * 4 + e);
                     w[q] &= ~(0xFFu << (8 * e));
                   }
               row[at] = make_uint4(w[0], w[1], w[2], w[3]);
             }
+            found |= bits;
+            if (p.L > 1) C->nan_bits[sb][me][chunk] = static_cast<uint16_t>(bits);
           }
         }
         if (p.L > 1) {
-          // bits of dims [half * D / 2, ...): two words with D = 128, one with D = 64
+          if (any == all) {
 #pragma unroll
-          for (int i = 0; i < D / 64; ++i) C->nan_bits[sb][me][half * (D / 64) + i] = bits[i];
+            for (int i = 0; i < CH; ++i) C->nan_bits[sb][me][part * CH + i] = 0;
+          }
           if (me % p.page == 0) C->nan_tok[sb][page_of] = tok;
-          if (bits[0] | bits[1]) C->nan_tile[sb] = static_cast<int>(t);
+          if (found) C->nan_tile[sb] = static_cast<int>(t);
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // P (and cleared values) are read by the MMA
@@ -835,7 +848,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
         if (!meet()) break;
         const int b = d.b, h = d.h, row0 = d.row0, rows = d.rows;
         const bool begins = d.seg || k0 == 0, whole = begins && d.left == 0;
-        float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + d.seg) * R * (D + 2);
+        float* left = p.part + (static_cast<size_t>(blockIdx.x) * 2 + d.seg) * R * (D + 2);
 #pragma unroll
         for (int c = 0; c < HC; ++c) {
           const int r = c0 + c;
@@ -848,7 +861,7 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
               if constexpr (HALF) reinterpret_cast<__half*>(p.out)[at] = __float2half_rn(o);
               else reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o);
             } else {
-              part[r * D + me] = acc[c];
+              left[r * D + me] = acc[c];
             }
           }
         }
@@ -857,13 +870,13 @@ __global__ void __launch_bounds__(C_THREADS, (CacheShape<D, R, HALF>::CTAS))
           const float4 v = *reinterpret_cast<const float4*>(C->sum[r]);
           const float sum = (v.x + v.y) + (v.z + v.w);
           if (!whole) {
-            part[R * D + r] = m;
-            part[R * D + R + r] = sum;
+            left[R * D + r] = m;
+            left[R * D + R + r] = sum;
           } else if (p.lse) {
             p.lse[C->out[qb][r]] = sum == 0.f ? ninf : (m + log2f(sum)) * LN2;
           }
         }
-        if (begins && !whole && me == 0 && half == 0) {
+        if (begins && !whole && me == 0 && part == 0) {
           // the unit goes on in the next CTAs: the joining kernel starts from here
           const long long end = C->stop - 1 + d.left;  // its last tile; CTA c holds tiles from c * total / n_cta on
           const int last_cta = static_cast<int>(((end + 1) * n_cta - 1) / C->total);
@@ -970,7 +983,7 @@ si_status launch_cache(CacheParams& p, const si_cache* c, int n_sm, const si_opt
   cudaError_t e = cudaFuncSetAttribute(cache_attention_kernel<D, R, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e == cudaSuccess) {
-    cache_attention_kernel<D, R, HALF><<<grid, C_THREADS, smem, stream>>>(tm_k, tm_v, p);
+    cache_attention_kernel<D, R, HALF><<<grid, Sh::THREADS, smem, stream>>>(tm_k, tm_v, p);
     if (p.cut) cache_join_kernel<D, R, HALF><<<dim3(grid, std::min(R, p.L * p.G)), 128, 0, stream>>>(p);
     e = cudaGetLastError();
   }
