@@ -116,6 +116,12 @@ __device__ __forceinline__ Span span_of(const CacheParams& p, int b) {
   return s;
 }
 
+// part * total / n, by a 32-bit division where that is enough.
+__device__ __forceinline__ long long share(long long total, unsigned part, unsigned n) {
+  const unsigned long long x = static_cast<unsigned long long>(total) * part;
+  return x >> 32 ? static_cast<long long>(x / n) : static_cast<long long>(static_cast<uint32_t>(x) / n);
+}
+
 __device__ __forceinline__ void cache_error(const CacheParams& p, volatile int* abort, int where) {
   atomicCAS(p.err, 0, static_cast<int>(SI_ERR_TIMEOUT));
   atomicCAS(p.err + 1, 0, where);
@@ -224,7 +230,6 @@ struct CacheCtrl {
   uint16_t nan_bits[2][C_TILE][D / 16];  // dims whose value is NaN, for tokens that only some rows see
   int nan_tok[2][8], nan_tile[2];     // first tokens of such a tile's pages, and its number
   long long scan[Sh::THREADS / 32];
-  long long total, start, stop;       // tiles of the batch; this CTA's run
   int b0;                             // the sequence in which the run starts,
   long long before0;                  // and the tiles of one (head, chunk) in the sequences before it
   uint32_t tmem_slot;
@@ -276,49 +281,48 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
 
   // ---- this CTA's run of tiles
   const int HN = p.H_kv * p.chunks;
+  long long total = 0, start = 0, stop_at = 0;
+  int n_cta = static_cast<int>(gridDim.x);
   if (p.cut) {
-    long long sum = 0;
-    for (int b = tid; b < p.B; b += C_THREADS) sum += span_of(p, b).tiles;
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) C->scan[warp] = sum;
-    __syncthreads();
-    if (tid == 0) {
-      long long t = 0;
-      for (int w = 0; w < C_THREADS / 32; ++w) t += C->scan[w];
-      t *= HN;
-      // fewer CTAs than the grid where their runs would get too short
-      const long long n = min(static_cast<long long>(gridDim.x), max(t / C_MIN_RUN, 1ll));
-      C->total = t;
-      C->start = blockIdx.x < n ? blockIdx.x * t / n : t;
-      C->stop = blockIdx.x < n ? (blockIdx.x + 1) * t / n : t;
-    }
-    __syncthreads();
-    // the sequence in which the run starts
-    long long run = 0;
-    const long long start = C->start;
-    for (int base = 0; base < p.B && start < C->total; base += C_THREADS) {
+    // prefix of the sequences' tiles over the block's threads; false: past the last one
+    long long before = 0, tiles = 0, run = 0;
+    auto scan = [&](int base) {
       const int b = base + tid;
-      const long long t = b < p.B ? span_of(p, b).tiles : 0;
-      long long inc = t;
+      tiles = b < p.B ? span_of(p, b).tiles : 0;
+      long long inc = tiles;
+#pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
         if (lane >= o) inc += u;
       }
+      __syncthreads();  // the last sums have been read
       if (lane == 31) C->scan[warp] = inc;
       __syncthreads();
-      long long before = run, all = run;
+      before = run;
+#pragma unroll
       for (int w = 0; w < C_THREADS / 32; ++w) {
-        if (w < warp) before += C->scan[w];
-        all += C->scan[w];
+        const long long v = C->scan[w];
+        if (w < warp) before += v;
+        run += v;
       }
-      before += inc - t;
-      if (t > 0 && before * HN <= start && start < (before + t) * HN) {
-        C->b0 = b;
+      before += inc - tiles;
+    };
+    for (int base = 0; base < p.B; base += C_THREADS) scan(base);
+    total = run * HN;
+    // fewer CTAs than the grid where their runs would get too short
+    n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total / C_MIN_RUN, 1ll)));
+    if (static_cast<int>(blockIdx.x) < n_cta) {
+      start = share(total, blockIdx.x, n_cta);
+      stop_at = share(total, blockIdx.x + 1, n_cta);
+    }
+    // the sequence in which the run starts (the scan of a small batch is still at hand)
+    if (p.B > C_THREADS) run = 0;
+    for (int base = 0; base < p.B; base += C_THREADS) {
+      if (p.B > C_THREADS) scan(base);
+      if (start < stop_at && tiles > 0 && before * HN <= start && start < (before + tiles) * HN) {
+        C->b0 = base + tid;
         C->before0 = before;
       }
-      run = all;
-      __syncthreads();
-      if (all * HN > start) break;
     }
   }
   tc_fence_before();
@@ -327,17 +331,15 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
   const uint32_t tmem = C->tmem_slot;
 
   // n_tiles of this CTA, the first at tile k0 of unit (b0, hn0)
-  const int n_cta = p.cut ? static_cast<int>(min(static_cast<long long>(gridDim.x), max(C->total / C_MIN_RUN, 1ll)))
-                          : static_cast<int>(gridDim.x);
   long long n_tiles = 0;
   int b0 = 0, hn0 = 0, k0 = 0;
   long long u_stop = 0;  // whole units: the run's end
   if (p.cut) {
-    n_tiles = C->stop - C->start;
+    n_tiles = stop_at - start;
     if (n_tiles > 0) {
       b0 = C->b0;
       const int t = span_of(p, b0).tiles;
-      const long long in_b = C->start - C->before0 * HN;
+      const long long in_b = start - C->before0 * HN;
       hn0 = static_cast<int>(in_b / t);
       k0 = static_cast<int>(in_b % t);
     }
@@ -556,61 +558,73 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
       }
       ++n_unit;
       const long long len = p.lens[b];
-      constexpr int E = D / 32;  // dims of a lane
-      constexpr int BATCH = R / 2 < 8 ? R / 2 : 8;  // rows whose loads are under way together
+      // eight lanes a row, four rows at a time, the loads of several steps under way together
+      constexpr int EL = D / 8, STEPS = R / 8 < 4 ? R / 8 : 4;  // a lane's dims
+      const int sub = lane & 7;
 #pragma unroll 1
-      for (int r0 = warp - 2; r0 < rows; r0 += 2 * BATCH) {
-        uint32_t raw[BATCH][E / 2];
+      for (int r0 = (warp - 2) * 4 + (lane >> 3); r0 - (lane >> 3) < rows; r0 += 8 * STEPS) {
+        uint4 raw[STEPS][EL / 8];
+        int row_i[STEPS], out_at[STEPS];
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-          const int row = row0 + min(r0 + 2 * j, rows - 1), i = row / p.G, g = row % p.G;
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(
-              p.q + ((((static_cast<size_t>(b) * p.L + i) * p.H) + h * p.G + g) * D + lane * E) * 2);
+        for (int j = 0; j < STEPS; ++j) {
+          const int row = row0 + min(r0 + 8 * j, rows - 1), i = row / p.G, g = row - i * p.G;
+          row_i[j] = i;
+          out_at[j] = (b * p.L + i) * p.H + h * p.G + g;
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(out_at[j]) * D + sub * EL) * 2);
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e) raw[j][e] = src[e];
+          for (int e = 0; e < EL / 8; ++e) raw[j][e] = src[e];
         }
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-        const int r = r0 + 2 * j;
-        if (r >= rows) break;
-        const int row = row0 + r, i = row / p.G, g = row % p.G;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < STEPS; ++j) {
+          const int r = r0 + 8 * j;
+          float v[EL], amax = 0.f;
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          float2 f;
-          if constexpr (HALF) f = __half22float2(*reinterpret_cast<const __half2*>(&raw[j][e]));
-          else f = make_float2(__uint_as_float(raw[j][e] << 16), __uint_as_float(raw[j][e] & 0xFFFF0000u));
-          v[2 * e] = f.x;
-          v[2 * e + 1] = f.y;
-        }
-        const float amax = warp_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
-        // 2^x, so that amax / 2^x is in [224, 448]: the exponent as it stands in a float
-        const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - ((__float_as_uint(amax) & 0x7FFFFFu) > 0x600000u ? 7 : 8);
-        const int exb = min(max(ex, 1), 253);
-        const float sc = __uint_as_float(static_cast<uint32_t>(exb) << 23);
-        const float inv = __uint_as_float(static_cast<uint32_t>(254 - exb) << 23);
+          for (int e = 0; e < EL / 2; ++e) {
+            const uint32_t w = reinterpret_cast<const uint32_t*>(raw[j])[e];
+            float2 f;
+            if constexpr (HALF) f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+            else f = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+            v[2 * e] = f.x;
+            v[2 * e + 1] = f.y;
+            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] *= inv;
-        // rows of D bytes, 16-byte chunks swizzled within 8-row atoms
-        const int byte = lane * E;
-        const int chunk = D == 128 ? (byte >> 4) ^ (r & 7) : (byte >> 4) ^ ((r >> 1) & 3);
-        uint8_t* dst = q_s + qb * Sh::Q + r * D + chunk * 16 + (byte & 15);  // (R is a multiple of 8: all terms swizzle alike)
+          for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+          // 2^x, so that amax / 2^x is in [224, 448]: the exponent as it stands in a float
+          const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - ((__float_as_uint(amax) & 0x7FFFFFu) > 0x600000u ? 7 : 8);
+          const int exb = min(max(ex, 1), 253);
+          const float sc = __uint_as_float(static_cast<uint32_t>(exb) << 23);
+          const float inv = __uint_as_float(static_cast<uint32_t>(254 - exb) << 23);
 #pragma unroll
-        for (int term = 0; term < TERMS; ++term) {
-          const uint32_t c = e4m3x4(v[0], v[1], v[2], v[3]);
-          if constexpr (E == 4) *reinterpret_cast<uint32_t*>(dst + term * R * D) = c;
-          else *reinterpret_cast<uint16_t*>(dst + term * R * D) = static_cast<uint16_t>(c);
-          take_off(v, c);
-        }
-        if (lane == 0) {
-          const long long pos = len - p.L + i;
-          const int ps = static_cast<int>(pos < 0 ? -1 : pos);
-          // e4m3 has no infinity: a row that holds one scores NaN
-          C->qs[qb][r] = amax <= 3.402823466e38f ? sc * p.scale_log2 : __int_as_float(0x7fc00000);
-          C->pos[qb][r] = ps;
-          C->low[qb][r] = p.window && p.window <= ps ? ps - p.window : -1;
-          C->out[qb][r] = (b * p.L + i) * p.H + h * p.G + g;
-        }
+          for (int e = 0; e < EL; ++e) v[e] *= inv;
+          if (r < rows) {
+            // rows of D bytes, 16-byte chunks swizzled within 8-row atoms (R is a
+            // multiple of 8: all terms of a row swizzle alike)
+            const int byte = sub * EL;
+            const int chunk = D == 128 ? (byte >> 4) ^ (r & 7) : (byte >> 4) ^ ((r >> 1) & 3);
+            uint8_t* dst = q_s + qb * Sh::Q + r * D + chunk * 16 + (byte & 15);
+#pragma unroll
+            for (int term = 0; term < TERMS; ++term) {
+              uint32_t c[EL / 4];
+#pragma unroll
+              for (int e = 0; e < EL / 4; ++e) {
+                float(&x)[4] = *reinterpret_cast<float(*)[4]>(v + 4 * e);
+                c[e] = e4m3x4(x[0], x[1], x[2], x[3]);
+                if (term + 1 < TERMS) take_off(x, c[e]);
+              }
+              if constexpr (EL == 16) *reinterpret_cast<uint4*>(dst + term * R * D) = make_uint4(c[0], c[1], c[2], c[3]);
+              else *reinterpret_cast<uint2*>(dst + term * R * D) = make_uint2(c[0], c[1]);
+            }
+            if (sub == 0) {
+              const long long pos = len - p.L + row_i[j];
+              const int ps = static_cast<int>(pos < 0 ? -1 : pos);
+              // e4m3 has no infinity: a row that holds one scores NaN
+              C->qs[qb][r] = amax <= 3.402823466e38f ? sc * p.scale_log2 : __int_as_float(0x7fc00000);
+              C->pos[qb][r] = ps;
+              C->low[qb][r] = p.window && p.window <= ps ? ps - p.window : -1;
+              C->out[qb][r] = out_at[j];
+            }
+          }
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read by the MMA
@@ -878,8 +892,8 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
         }
         if (begins && !whole && me == 0 && part == 0) {
           // the unit goes on in the next CTAs: the joining kernel starts from here
-          const long long end = C->stop - 1 + d.left;  // its last tile; CTA c holds tiles from c * total / n_cta on
-          const int last_cta = static_cast<int>(((end + 1) * n_cta - 1) / C->total);
+          const long long end = stop_at - 1 + d.left;  // its last tile; CTA c holds tiles from c * total / n_cta on
+          const int last_cta = static_cast<int>(((end + 1) * n_cta - 1) / total);
           p.meta[blockIdx.x] = make_int4(b, h * p.chunks + row0 / R, last_cta - static_cast<int>(blockIdx.x) + 1, d.seg);
         }
         __syncwarp();
