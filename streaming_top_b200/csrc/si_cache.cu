@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(256, 4) cache_append_kernel(const AppendParams
   const long long len = p.lens[b];
   const long long nn = p.n_new ? min(max(p.n_new[b], 0), p.L) : p.L;
   const long long start = len > 0 ? len : 0, stop = len + nn;  // tokens written: [start, stop)
-  const long long pg = start / p.page + slot, t0 = pg * p.page;
+  const int shift = 31 - __clz(p.page);  // (a power of two)
+  const long long pg = (start >> shift) + slot, t0 = pg << shift;
   const long long lo = max(start, t0), hi = min(stop, t0 + p.page);
   if (lo >= hi || pg >= p.max_pages) return;
   const int id = p.table[static_cast<size_t>(b) * p.max_pages + pg];
@@ -90,7 +91,6 @@ __global__ void __launch_bounds__(256, 4) cache_append_kernel(const AppendParams
   const float old = off > 0 ? *scale : 0.f;
 
   uint4 x[AP_VECS];
-  float amax = 0.f;
 #pragma unroll
   for (int j = 0; j < AP_VECS; ++j) {
     const int vec = threadIdx.x + j * blockDim.x, row = vec / VROW;
@@ -98,16 +98,28 @@ __global__ void __launch_bounds__(256, 4) cache_append_kernel(const AppendParams
     if (row < cnt)
       x[j] = __ldcs(reinterpret_cast<const uint4*>(rows + static_cast<size_t>(row) * p.H_kv * (D * 2) + (vec % VROW) * 16));
   }
+  // the largest magnitude: 16-bit patterns without their sign order as their values
+  constexpr uint32_t LIMIT = HALF ? 0x7C00u : 0x7F80u;  // infinity; NaN above
+  uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < AP_VECS; ++j) {
-    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = to_float2<HALF>(w[i]);
-      const float a = fabsf(f.x), c = fabsf(f.y);
-      amax = fmaxf(amax, fmaxf(a <= 3.402823466e38f ? a : 0.f, c <= 3.402823466e38f ? c : 0.f));
+  for (int j = 0; j < AP_VECS; ++j)
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[j].x & 0x7FFF7FFFu, x[j].y & 0x7FFF7FFFu),
+                                 __vmaxu2(x[j].z & 0x7FFF7FFFu, x[j].w & 0x7FFF7FFFu)));
+  top = max(top & 0xFFFFu, top >> 16);
+  if (top >= LIMIT) {  // not finite: once more, without those
+    top = 0;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < cnt * D / 2; i += blockDim.x) {
+      // the thread's own vectors, word by word
+      const int vec = threadIdx.x + (i / static_cast<int>(blockDim.x) / 4) * blockDim.x, row = vec / VROW;
+      if (row >= cnt) break;
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(rows + static_cast<size_t>(row) * p.H_kv * (D * 2) + (vec % VROW) * 16 +
+                                                            (i / static_cast<int>(blockDim.x) % 4) * 4);
+      const uint32_t lo16 = w & 0x7FFFu, hi16 = (w >> 16) & 0x7FFFu;
+      top = max(top, max(lo16 < LIMIT ? lo16 : 0u, hi16 < LIMIT ? hi16 : 0u));
     }
   }
+  const float amax = to_float2<HALF>(top).x;
   const uint32_t wm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax));  // non-negative: bits order as values
   if ((threadIdx.x & 31) == 0) s_amax[threadIdx.x >> 5] = wm;
   __syncthreads();
@@ -133,20 +145,25 @@ __global__ void __launch_bounds__(256, 4) cache_append_kernel(const AppendParams
       *at = make_uint4(r[0], r[1], r[2], r[3]);
     }
   }
+  if (pow2) {
 #pragma unroll
-  for (int j = 0; j < AP_VECS; ++j) {
-    const int vec = threadIdx.x + j * blockDim.x, row = vec / VROW;
-    if (row >= cnt) break;
-    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = to_float2<HALF>(w[i]);
-      f[2 * i] = pow2 ? t.x * inv : t.x / s;
-      f[2 * i + 1] = pow2 ? t.y * inv : t.y / s;
+    for (int j = 0; j < AP_VECS; ++j) {
+      const int vec = threadIdx.x + j * blockDim.x, row = vec / VROW;
+      if (row < cnt) {
+        const float2 a = to_float2<HALF>(x[j].x), b = to_float2<HALF>(x[j].y), c = to_float2<HALF>(x[j].z),
+                     d = to_float2<HALF>(x[j].w);
+        *reinterpret_cast<uint2*>(codes + static_cast<size_t>(off + row) * D + (vec % VROW) * 8) =
+            make_uint2(encode4(a.x * inv, a.y * inv, b.x * inv, b.y * inv), encode4(c.x * inv, c.y * inv, d.x * inv, d.y * inv));
+      }
     }
-    *reinterpret_cast<uint2*>(codes + static_cast<size_t>(off + row) * D + (vec % VROW) * 8) =
-        make_uint2(encode4(f[0], f[1], f[2], f[3]), encode4(f[4], f[5], f[6], f[7]));
+  } else {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < cnt * (D / 4); i += blockDim.x) {
+      const int row = i / (D / 4), at = i % (D / 4);
+      const uint2 w = *reinterpret_cast<const uint2*>(rows + static_cast<size_t>(row) * p.H_kv * (D * 2) + at * 8);
+      const float2 a = to_float2<HALF>(w.x), b = to_float2<HALF>(w.y);
+      *reinterpret_cast<uint32_t*>(codes + static_cast<size_t>(off + row) * D + at * 4) = encode4(a.x / s, a.y / s, b.x / s, b.y / s);
+    }
   }
 }
 
