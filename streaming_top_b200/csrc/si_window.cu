@@ -761,8 +761,14 @@ __global__ void __launch_bounds__(W_THREADS, 1)
 // Q and K are free once both S are there, so the next item's arrive during the
 // softmax, V's during the next QK.
 //
-// Measured on window 128, 4 sinks, 64 / 8 heads, D = 128, 16,384 positions:
-// BANDFIGURES
+// Window 128, 4 sinks, 64 query and 8 key/value heads, D = 128, 16,384
+// positions: 188 us (3.2 TB/s of 6.5, 22 % of the bf16 rate); the streaming
+// form 276 us.  What is left is latency: a query tile's QK, softmax, PV and
+// epilogue follow one another (1.3, 4, 1.4 and 2.7 thousand clocks), and with
+// O over S only two fit into tensor memory.  Without the stores it takes 34 us
+// less, without the exponentials 18.  Tried and not faster: two warpgroups a
+// query tile that share its columns (232 us) or take items in turn (194 us),
+// a share of the exponentials on the FMA units (177 to 194 against 177 us).
 
 struct BandItem {
   int b, h, p0, len, k_start, sink_end;
@@ -841,8 +847,9 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       prefetch_tmap(&tm_v);
       uint32_t i = 0;
       bool v_began = false;
-      for (int n = blockIdx.x; n < p.items; n += gridDim.x, ++i) {
+      for (int n = blockIdx.x; n < p.items; n += gridDim.x) {
         const BandItem it = band_item(p, n);
+        if (it.p0 >= it.len) continue;  // padding alone
         if (!mbar_wait_bounded(&C->qk_empty, (i & 1u) ^ 1u, abort, limit)) {
           window_error(p, abort, WERR_Q);
           break;
@@ -865,6 +872,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
           tma_load_4d(v_s + c * plane + s16 * 128, &tm_v, &C->v_full, c * 64, it.h, it.k_start, it.b);
         }
         v_began = true;
+        ++i;
       }
       // every copy issued has landed before the CTA can exit
       bool ok = !i || mbar_wait_timed(&C->qk_full, (i - 1) & 1u, limit);
@@ -885,8 +893,10 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     };
     uint32_t i = 0;
     bool stop = false;
-    for (int n = blockIdx.x; n < p.items && !stop; n += gridDim.x, ++i) {
-      const uint32_t par = i & 1u;
+    for (int n = blockIdx.x; n < p.items && !stop; n += gridDim.x) {
+      const BandItem it = band_item(p, n);
+      if (__all_sync(0xFFFFFFFFu, it.p0 >= it.len)) continue;
+      const uint32_t par = i++ & 1u;
       if (!await(&C->qk_full, par, WERR_Q)) break;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
@@ -928,8 +938,9 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     // ------------------------------------------------------------ value check
     constexpr uint32_t EXP = HALF ? 0x7C007C00u : 0x7F807F80u, CARRY = HALF ? 0x04000400u : 0x00800080u;
     uint32_t i = 0;
-    for (int n = blockIdx.x; n < p.items; n += gridDim.x, ++i) {
+    for (int n = blockIdx.x; n < p.items; n += gridDim.x) {
       const BandItem it = band_item(p, n);
+      if (it.p0 >= it.len) continue;
       const int last = min(it.p0 + 2 * p.P, it.len) - 1;
       // the last item's verdict has been read, this one's values are here
       const bool got = mbar_wait_bounded(&C->checked, (i & 1u) ^ 1u, abort, limit) &&
@@ -961,6 +972,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // cleared values are read by the MMA
       __syncwarp();
       if (lane == 0) mbar_arrive(&C->v_ok);
+      ++i;
     }
   } else {
     // ------------------------------------------------------------ softmax and epilogue of a query tile
@@ -972,10 +984,18 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     uint8_t* stage = o_s + (warp - 4) * BAND_STAGE;
     const int chunks = (keys + 63) / 64;
     uint32_t i = 0;
-    for (int n = blockIdx.x; n < p.items; n += gridDim.x, ++i) {
+    for (int n = blockIdx.x; n < p.items; n += gridDim.x) {
       const BandItem it = band_item(p, n);
-      const uint32_t par = i & 1u;
       const int pos = it.p0 + m * p.P + i_pos;
+      if (it.p0 >= it.len) {
+        if (used && pos < p.S) {
+          const size_t at = (static_cast<size_t>(it.b) * p.S + pos) * p.H + it.h * p.G + head_of;
+          for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(p.out + at * (D * 2) + c * 16) = make_uint4(0, 0, 0, 0);
+          if (p.lse) p.lse[at] = ninf;
+        }
+        continue;
+      }
+      const uint32_t par = i & 1u;
       const bool live = used && pos < it.len;
       // seen: columns up to b that lie behind a, or before e; of the sinks' columns those before sink_end
       const int b = pos - it.k_start + s16, a = b - p.window, e = p.n_sink - it.k_start + s16;
@@ -1114,6 +1134,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
           if (rp < it.len) row_by_keys<D, HALF>(p, full, rp, it.h * p.G + r % p.G);
         }
       }
+      ++i;
     }
   }
 
@@ -1176,8 +1197,12 @@ si_status launch_window_tiles(WindowParams& p, int n_sm, cudaStream_t stream) {
     return launch_tiles(band_attention_kernel<D, HALF>, smem, p, D, HALF, p.band_keys - p.band_sinks,
                         std::max(p.band_sinks, 16), n_sm, stream);
   }
-  // a query tile sees window + P - 1 keys
-  if (p.window + p.P <= 320) return launch_window<D, HALF, 64>(p, n_sm, stream);
+  // A query tile sees window + P - 1 keys.  Tiles of 64 keys waste fewer columns
+  // at the band's ends and keep two S buffers, but their QK takes as long as
+  // that of 128.  16,384 positions, 64 heads, P = 16, tiles of 64 against 128:
+  // window 256 369 and 398 us, 384 424 and 428, 512 519 and 485, 2048 672 and 482
+  // (8192 positions, 32 heads); window 128 with a head each (P = 128) 357 and 383.
+  if (p.window + p.P <= 400) return launch_window<D, HALF, 64>(p, n_sm, stream);
   return launch_window<D, HALF, 128>(p, n_sm, stream);
 }
 
@@ -1224,7 +1249,8 @@ si_status si_window_attention(const void* q, const void* k, const void* v, const
   p.items = B * H_kv * p.blocks;
   p.wide_out = aligned(out, 32);
   p.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(D))) * LOG2E;
-  p.wait_limit_ns = kDefaultWaitLimitNs;
+  // (an item that is done again key by key holds up its CTA for some 10 us a key at most)
+  p.wait_limit_ns = kDefaultWaitLimitNs + static_cast<uint64_t>(S) * 10000;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool half = dtype == SI_DTYPE_FP16;
   if (D == 128) return half ? launch_window_tiles<128, true>(p, n_sm, s) : launch_window_tiles<128, false>(p, n_sm, s);
