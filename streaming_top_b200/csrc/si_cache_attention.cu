@@ -29,6 +29,16 @@
 // kernel joins.  Where a unit has few tiles at most, units are not cut and no
 // second kernel is launched.
 //
+// Measured (D = 128 unless said; bytes are those of the visible codes): 64
+// sequences of 4096 to 8192 tokens, 64 / 8 heads: 150 us, 5.4 TB/s of 6.5; 16
+// of 8192 to 16,384 tokens, four queries each, 32 / 8 heads, D = 64, fp16: 115 us,
+// 1.8 TB/s; one of 262,143 tokens, 64 / 1 heads: 78 us, 0.86 TB/s; windows of 128
+// tokens and 4 sinks in 128 sequences: 33 us.  With eight rows a head a tile
+// takes 2700 clocks in each of an SM's two CTAs, near the 1400 that its bytes
+// need; with more rows, or few tiles a CTA, the hand-offs between the warps (a
+// tile's S, maximum, P, O) are what is left: without the exponentials, the
+// rounding to terms and the maxima, 64 rows take 93 instead of 98 us.
+//
 // Warps: 0 schedules (walks the tiles, reads page table and scales ahead,
 // publishes tile descriptors) and loads pages by TMA; 1 issues the MMAs; 2-3
 // split the queries into terms; the rest do the softmax: two or four
@@ -54,9 +64,12 @@ namespace {
 
 constexpr int C_TILE = 128;      // tokens of a tile
 constexpr int C_ND = 8;          // tile descriptors in flight
-constexpr int C_WHOLE = 4;       // units of at most this many tiles are not cut
+// Units of at most this many tiles are not cut: the second kernel costs more
+// than their length.  64 query and 8 key/value heads, cut against whole: 1000
+// tokens (8 tiles) 22 and 18 us a sequence, 45 and 38 us for 64 of them; 2000
+// tokens (16 tiles) 21.5 and 27.
+constexpr int C_WHOLE = 8;
 constexpr int C_MAX_CTAS = 512;  // of a launch
-constexpr int C_MIN_RUN = 2;     // tiles a CTA gets at least when units are cut
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 enum { CERR_SLOT = 41, CERR_DESC = 42, CERR_FULL = 43, CERR_Q = 44, CERR_S = 45, CERR_P = 46, CERR_O = 47,
@@ -309,8 +322,7 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
     };
     for (int base = 0; base < p.B; base += C_THREADS) scan(base);
     total = run * HN;
-    // fewer CTAs than the grid where their runs would get too short
-    n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total / C_MIN_RUN, 1ll)));
+    n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), total));  // (every sequence has a tile)
     if (static_cast<int>(blockIdx.x) < n_cta) {
       start = share(total, blockIdx.x, n_cta);
       stop_at = share(total, blockIdx.x + 1, n_cta);

@@ -621,3 +621,171 @@ def test_refusals_leave_the_context_usable():
         si.cache_reserve(cache, t, l, r, _i32([20]).cuda())
     assert e.value.status == si.SI_ERR_OUT_OF_MEMORY
     assert si.cache_reserve(cache, t, l, r, _i32([10]).cuda()).item() == 0
+
+
+def test_offsets_past_32_bits():
+    """Pools of more than 2^32 bytes: append, attention, fork and compaction at their far end."""
+    g = _gen(31)
+    page, G, D, H, n = 128, 8, 128, 16, 300
+    n_pages = (1 << 32) // (G * page * D) + 40
+    kp = torch.zeros((n_pages, G, page, D), dtype=torch.uint8, device="cuda")
+    vp = torch.zeros_like(kp)
+    ks, vs = [torch.zeros((n_pages, G), device="cuda") for _ in range(2)]
+    cache = si.PagedCache(kp, vp, ks, vs)
+    table = _i32([[n_pages - 1, n_pages - 7, n_pages - 3, -1], [-1] * 4]).cuda()
+    refs = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+    refs[table[0, :3].long()] = 1
+    refs[: n_pages - 20] = 1  # all but the last pages are taken
+    x = torch.randn((2, n, G, D), generator=g).bfloat16().cuda()
+    lens = _i32([0, 0]).cuda()
+    si.cache_append(cache, x, -x, table, lens, n_new=_i32([n, 0]).cuda())
+    lens = _i32([n, 0]).cuda()
+    q = torch.randn((2, 1, H, D), generator=g).bfloat16().cuda()
+
+    def check(out, lse):
+        ids = table.unique()
+        ids = ids[ids >= 0].long()
+        small = torch.searchsorted(ids, table.long()).int()
+        small[table < 0] = -1
+        pool = [t[ids].cpu() for t in (kp, vp, ks, vs)]
+        want = ref.cache_attention(q.cpu(), *pool, small.cpu(), lens.cpu())
+        ref.check((out, lse), want, STEP["cache"], 448.0 * pool[3].max().item(), n)
+
+    check(*si.cache_attention(q, cache, table, lens))
+    assert si.cache_fork(cache, table, lens, refs, _i32([0]).cuda(), _i32([1]).cuda()).item() == 0
+    assert int(table[1, 2]) == n_pages - 20 and int(lens[1]) == n
+    a = si.cache_attention(q, cache, table, lens)
+    check(*a)
+    refs[:4] = 0
+    si.cache_compact(cache, table, refs)
+    b = si.cache_attention(q, cache, table, lens)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert si.device_status() == si.SI_OK
+
+
+def test_own_workspace_and_status_word():
+    g = _gen(32)
+    pool = _cuda(*_pool(60, 2, 64, 128, g))
+    cache = si.PagedCache(*pool)
+    table = _table([3000], 60, 64, 60, g).cuda()
+    lens = _i32([3000]).cuda()
+    q = torch.randn((1, 1, 64, 128), generator=g).half().cuda()
+    want = si.cache_attention(q, cache, table, lens)
+    ws = torch.empty(si.cache_attention_workspace_size(128), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    si.test_fail_allocations(1)  # with its own workspace the call allocates nothing
+    got = si.cache_attention(q, cache, table, lens, workspace=ws, device_status=status)
+    with pytest.raises(si.SIError):
+        si.cache_attention(q, cache, table, lens)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1]) and status.eq(0).all()
+    q, k, v = _cuda(*_qkv(1, 100, 4, 2, 64, torch.float16, 33))
+    si.window_attention(q, k, v, window=10, device_status=status)
+    assert status.eq(0).all()
+
+
+def test_outputs_aligned_to_16_bytes_only():
+    """Slices of a larger buffer, 16 but not 32 bytes aligned."""
+    q, k, v = _cuda(*_qkv(1, 300, 4, 2, 64, torch.bfloat16, 34))
+    for window in (20, 300):
+        want = si.window_attention(q, k, v, window=window)
+        flat = torch.full((q.numel() + 16,), 7.0, dtype=q.dtype, device="cuda")
+        out = flat[8: 8 + q.numel()].view_as(q)
+        assert out.data_ptr() % 32 == 16
+        si.window_attention(q, k, v, window=window, out=out)
+        assert torch.equal(out, want[0])
+        assert (flat[:8] == 7).all() and (flat[-8:] == 7).all()
+
+
+def test_page_calls_captured():
+    """Reserve, fork, free and compact in one graph, replayed from the same state: the same result as eagerly."""
+    g = _gen(35)
+    page, n_pages = 16, 300
+    pool = _cuda(*_pool(n_pages, 2, page, 64, g))
+    table, lens, refs = _state(40, 12, n_pages, page, g)
+    empty = [b for b in range(40) if lens[b] == 0][:3]
+    full = [b for b in range(40) if lens[b] > 0][:3]
+    state = _cuda(_i32(table), _i32(lens), _i32(refs))
+    work = [t.clone() for t in state]
+    src, dst, rows = _cuda(_i32(full), _i32(empty), _i32(full[:1]))
+    new = torch.full((40,), 5, dtype=torch.int32, device="cuda")
+    cache = si.PagedCache(*pool)
+
+    def step():
+        t, l, r = work
+        a = si.cache_fork(cache, t, l, r, src, dst)
+        b = si.cache_reserve(cache, t, l, r, new)
+        si.cache_free(cache, t, l, r, rows)
+        return (a, b) + si.cache_compact(cache, t, r)
+
+    first = [t.clone() for t in pool]
+    want = [t.clone() for t in step()] + [t.clone() for t in work + pool]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        got = step()
+    for _ in range(2):
+        for t, v in zip(work + pool, state + first):
+            t.copy_(v)
+        gr.replay()
+        for a, b in zip(list(got) + work + pool, want):
+            assert torch.equal(a, b)
+
+
+def test_many_sequences():
+    """More sequences than a block has threads, most of them short, and more units than CTAs."""
+    g = _gen(36)
+    B, page = 700, 16
+    lens = [(7 * b) % 40 for b in range(B)]
+    lens[333] = 2500
+    n_pages = sum(-(-n // page) for n in lens)
+    pool = _pool(n_pages, 2, page, 64, g)
+    table = _table(lens, -(-2500 // page), page, n_pages, g)
+    q = torch.randn((B, 1, 4, 64), generator=g).bfloat16()
+    _check_cache(pool, q, table, _i32(lens))
+    _check_cache(pool, q, table, _i32(lens), window=30, n_sink=1)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_window_attention_wide(dtype, D):
+    """Key tiles of 128, sinks of a tile of their own (20) and of a small one (7), a padded batch."""
+    q, k, v = _qkv(2, 900, 4, 1, D, dtype, 40)
+    _check_window(q, k, v, 450, 7)
+    _check_window(q, k, v, 600, 20, _i32([900, 711]), poison=True)  # (writes NaN into the padding)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("window,n_sink,down", [(40, 3, False), (128, 0, False), (300, 0, False), (500, 5, False),
+                                                (128, 4, True), (500, 0, True)])
+def test_window_attention_scores_that_grow(dtype, window, n_sink, down):
+    """Scores that climb by some 40 along the keys (or fall): the running
+    maximum leaves its reference again and again, in the narrow form and in
+    both tile sizes of the streaming one."""
+    g = _gen(41)
+    S, H, D = 700, 8, 128
+    q = torch.randn((1, S, H, D), generator=g) * 0.05
+    k = torch.randn((1, S, 1, D), generator=g) * 0.05
+    v = torch.randn((1, S, 1, D), generator=g)
+    q[..., 0] = 8.0
+    ramp = torch.arange(S) / S
+    k[0, :, 0, 0] = 60.0 * (1 - ramp if down else ramp)
+    _check_window(q.to(dtype), k.to(dtype), v.to(dtype), window, n_sink)
+
+
+@pytest.mark.parametrize("down", [False, True])
+def test_cache_attention_scores_that_grow(down):
+    """The same over a cache of several tiles, cut between CTAs."""
+    g = _gen(42)
+    page, D, n = 64, 128, 3000
+    n_pages = -(-n // page)
+    kp, vp, ks, vs = _pool(n_pages, 1, page, D, g)
+    table = _table([n], n_pages, page, n_pages, g)
+    order = table[0].tolist()
+    ks = torch.full((n_pages, 1), 2.0 ** -8)
+    for j, p in enumerate(order):  # the first dim's code grows with the page
+        x = 400.0 * ((n_pages - 1 - j) if down else j) / n_pages
+        kp[p, :, :, 0] = torch.tensor(x).to(torch.float8_e4m3fn).view(torch.uint8)
+    q = torch.randn((1, 1, 8, D), generator=g) * 0.1
+    q[..., 0] = 200.0
+    _check_cache((kp, vp, ks, vs), q.bfloat16(), table, _i32([n]))
