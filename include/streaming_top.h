@@ -346,7 +346,9 @@ SI_API si_status si_cache_append(const si_cache* cache, const void* k, const voi
  * SI_DTYPE_FP16.  H a multiple of H_kv, H / H_kv <= 128; L >= 1; window and
  * n_sink >= 0.  Scratch for partial results is taken from opt->workspace when
  * it is given and large enough (si_cache_attention_workspace_size()), else
- * allocated on `stream`; opt->device_status is honoured, opt may be NULL.
+ * allocated on `stream`; calls that share a workspace belong on one stream
+ * (captured ones too: graphs that share one must not run at once).
+ * opt->device_status is honoured, opt may be NULL.  max_pages * page < 2^31 - 256.
  */
 SI_API si_status si_cache_attention(const void* q, const si_cache* cache, const int32_t* table,
                                     const int32_t* lens, int B, int L, int H, int max_pages, int window,

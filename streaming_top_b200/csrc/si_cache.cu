@@ -257,24 +257,25 @@ __device__ void list_pages(PlanShared* S, const int32_t* refs, int lo, int hi, b
   }
 }
 
-// Leading entries of a row (up to `most`) that are pages, counted by a warp.
-__device__ int leading_pages(const int32_t* row, int most, int n_pages) {
+// Leading entries of a row (up to `most`) that are pages, counted by a warp;
+// `first` is the row's entry at the lane.
+__device__ int leading_pages(const int32_t* row, int first, int most, int n_pages) {
   const int lane = threadIdx.x & 31;
-  int have = 0;
   for (int base = 0; base < most; base += 32) {
     const int j = base + lane;
-    const int id = j < most ? row[j] : -1;
+    const int id = j < most ? (base ? row[j] : first) : -1;
     const uint32_t bad = __ballot_sync(0xFFFFFFFFu, id < 0 || id >= n_pages);
-    if (bad) return have + __ffs(bad) - 1;
-    have += 32;
+    if (bad) return base + __ffs(bad) - 1;
   }
-  return min(have, most);
+  return most;
 }
 
 // Reserve (FORK false): need[i] new pages for row i.  Fork: need[i] copied
 // pages for pair i.  Both: validate and count the needs, spread over the
 // cluster; prefix them in order; list as many free pages as are needed; hand
 // them out.  need, held and the lengths live in every block's shared memory.
+// Bound by the latency of dependent loads, so what does not depend on another
+// load is under way with it.
 template <bool FORK>
 __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_T, 1) page_plan_kernel(const PageParams p) {
   extern __shared__ int dyn[];
@@ -285,34 +286,39 @@ __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_T, 1) page_
   int* need = dyn;            // [n] pages to hand out; -1: status 2
   int* held = dyn + p.n;      // [n] reserve: pages held; fork: pages of the child
   int* tok = dyn + 2 * p.n;   // [n] fork: tokens of the child
+  int* dsts = dyn + 3 * p.n;  // [n] fork: the destinations
+  if (FORK)
+    for (int i = threadIdx.x; i < p.n; i += PG_T) dsts[i] = p.dst[i];
   cl.sync();                  // every block runs before any writes into another's shared memory
-  count_free(cl, &S, p.refs, p.n_pages);
+  count_free(cl, &S, p.refs, p.n_pages);  // (its barriers also order dsts)
   for (int i = gw; i < p.n; i += n_gw) {
     int nd = 0, hd = 0, tk = 0;
     if (FORK) {
-      const int s = p.src[i], d = p.dst[i];
+      const int s = p.src[i], d = dsts[i];
       bool ok = s >= 0 && s < p.n_seq && d >= 0 && d < p.n_seq;
-      if (ok) {
-        const int d0 = p.table[static_cast<size_t>(d) * p.max_pages];
-        ok = p.lens[d] == 0 && (d0 < 0 || d0 >= p.n_pages);
-      }
       bool twice = false;
-      for (int j = lane; j < i; j += 32) twice |= p.dst[j] == d;
-      ok = ok && !__any_sync(0xFFFFFFFFu, twice);
       if (ok) {
+        const int32_t* row = p.table + static_cast<size_t>(s) * p.max_pages;
+        const int first = lane < p.max_pages ? row[lane] : -1;
+        const int d0 = p.table[static_cast<size_t>(d) * p.max_pages], d_len = p.lens[d];
         tk = max(p.lens[s], 0);
+        ok = d_len == 0 && (d0 < 0 || d0 >= p.n_pages);
+        for (int j = lane; j < i; j += 32) twice |= dsts[j] == d;
         const int most = static_cast<int>(min(static_cast<long long>(p.max_pages), (static_cast<long long>(tk) + p.page - 1) / p.page));
-        hd = leading_pages(p.table + static_cast<size_t>(s) * p.max_pages, most, p.n_pages);
+        hd = leading_pages(row, first, most, p.n_pages);
         tk = static_cast<int>(min(static_cast<long long>(tk), static_cast<long long>(hd) * p.page));
         nd = p.share ? (tk % p.page ? 1 : 0) : hd;
-      } else {
+      }
+      if (__any_sync(0xFFFFFFFFu, twice) || !ok) {
         nd = -1;
+        hd = tk = 0;
       }
     } else {
-      const int add = p.n_new[i];
+      const int32_t* row = p.table + static_cast<size_t>(i) * p.max_pages;
+      const int add = p.n_new[i], len = p.lens[i], first = lane < p.max_pages ? row[lane] : -1;
       if (add > 0) {
-        hd = leading_pages(p.table + static_cast<size_t>(i) * p.max_pages, p.max_pages, p.n_pages);
-        const long long want = (max(static_cast<long long>(p.lens[i]) + add, 0ll) + p.page - 1) / p.page;
+        hd = leading_pages(row, first, p.max_pages, p.n_pages);
+        const long long want = (max(static_cast<long long>(len) + add, 0ll) + p.page - 1) / p.page;
         nd = want > p.max_pages ? -1 : static_cast<int>(max(want - hd, 0ll));
       }
     }
@@ -524,7 +530,7 @@ bool ints_aligned(std::initializer_list<const void*> ps) {
   return true;
 }
 
-// Shared memory of the plan: three ints for each of n entries.
+// Shared memory of the plan: four ints for each of n entries.
 template <bool FORK>
 si_status launch_plan(PageParams& p, const si_cache* c, cudaStream_t stream) {
   // scratch: the free list, and for a fork the copies' ends and their count
@@ -536,9 +542,9 @@ si_status launch_plan(PageParams& p, const si_cache* c, cudaStream_t stream) {
   p.count = p.list + p.n_pages;
   p.from = p.count + 1;
   p.to = p.from + p.n_pages;
-  const size_t smem = static_cast<size_t>(p.n) * 3 * sizeof(int);
+  const size_t smem = static_cast<size_t>(p.n) * 4 * sizeof(int);
   cudaError_t e = cudaFuncSetAttribute(page_plan_kernel<FORK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       PG_MAX_ROWS * 3 * static_cast<int>(sizeof(int)));
+                                       PG_MAX_ROWS * 4 * static_cast<int>(sizeof(int)));
   if (e == cudaSuccess) {
     page_plan_kernel<FORK><<<PG_CTAS, PG_T, smem, stream>>>(p);
     e = cudaGetLastError();

@@ -199,9 +199,11 @@ def fork(table, lens, refs, src, dst, page, share):
     table, lens, refs = [list(r) for r in table], list(lens), list(refs)
     n_pages, width, n_seq = len(refs), len(table[0]), len(table)
     free = [p for p in range(n_pages) if refs[p] <= 0]
-    run, status, copies = 0, [], []
-    for i, (s, d) in enumerate(zip(src, dst)):
-        if not (0 <= s < n_seq and 0 <= d < n_seq) or lens0[d] != 0 or leading(before[d], n_pages) or d in dst[:i]:
+    run, status, copies, named = 0, [], [], set()
+    for s, d in zip(src, dst):
+        again = d in named
+        named.add(d)
+        if not (0 <= s < n_seq and 0 <= d < n_seq) or lens0[d] != 0 or leading(before[d], n_pages) or again:
             status.append(2)
             continue
         n = max(lens0[s], 0)

@@ -206,6 +206,54 @@ def test_fork(n_seq, width, n_pages, page, share):
         assert torch.equal(got.cpu(), want)
 
 
+def test_page_calls_at_their_largest():
+    """8192 rows and pairs, pools of more pages than a block scans at once, pages that run out half way."""
+    n_seq, page = 8192, 16
+    rng = random.Random(5)
+    for n_pages, width in ((30000, 3), (9000, 2)):
+        g = _gen(n_pages)
+        pool = _pool(n_pages, 1, page, 64, g)
+        cache = si.PagedCache(*_cuda(*pool))
+        ids = list(range(n_pages))
+        rng.shuffle(ids)
+        table, lens, refs = [[-1] * width for _ in range(n_seq)], [0] * n_seq, [0] * n_pages
+        for b in range(n_seq // 2):
+            lens[b] = rng.randint(0, 2 * page)
+            for j in range(-(-lens[b] // page)):
+                if not ids:
+                    break
+                table[b][j] = ids.pop()
+                refs[table[b][j]] = 1
+        src = [rng.randrange(n_seq // 2) for _ in range(n_seq)]
+        dst = [n_seq // 2 + i if i < n_seq // 2 else rng.randrange(n_seq) for i in range(n_seq)]
+        want = ref.fork(table, lens, refs, src, dst, page, True)
+        t, l, r = _cuda(_i32(table), _i32(lens), _i32(refs))
+        st = si.cache_fork(cache, t, l, r, _i32(src).cuda(), _i32(dst).cuda())
+        _same(st, want[3])
+        _same(t, want[0])
+        _same(l, want[1])
+        _same(r, want[2])
+        new = [rng.randint(-1, 2 * page) for _ in range(n_seq)]
+        wt, wr, ws = ref.reserve(want[0], want[1], want[2], new, page)
+        _same(si.cache_reserve(cache, t, l, r, _i32(new).cuda()), ws)
+        _same(t, wt)
+        _same(r, wr)
+        gone = [b for b in range(n_seq) if rng.random() < 0.5]
+        wt, wl, wr = ref.free(wt, want[1], wr, gone)
+        si.cache_free(cache, t, l, r, _i32(gone).cuda())
+        wt, wr, wu, wm, copies = ref.compact(wt, wr)
+        before = [x.cpu() for x in (cache.k_pages, cache.v_scale)]
+        used, moved = si.cache_compact(cache, t, r)
+        assert used.item() == wu
+        _same(moved, wm)
+        _same(t, wt)
+        _same(r, wr)
+        a, b = torch.tensor([c[0] for c in copies]), torch.tensor([c[1] for c in copies])
+        for x, y in zip(before, (cache.k_pages, cache.v_scale)):
+            x[b] = x[a]
+            assert torch.equal(x, y.cpu())
+
+
 def test_fork_runs_out_of_pages():
     """Pairs in order: the first that does not fit and those behind it fail, except the ones that need nothing."""
     page, n_pages = 16, 10
