@@ -40,6 +40,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -1181,6 +1182,18 @@ si_status launch_window(const WindowParams& p, int n_sm, cudaStream_t stream) {
   using Sh = WindowShape<D, KT>;
   constexpr size_t smem = 1024 + 2 * Sh::QT + (Sh::NK + Sh::NV) * Sh::TILE + sizeof(WindowCtrl<D, KT>);
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  // the kernel's register split has to fit the registers it is launched with,
+  // a property of the build: its warps would wait for the rest forever
+  static std::atomic<int> built{0};
+  int regs = built.load();
+  if (regs == 0) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, window_attention_kernel<D, HALF, KT>);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes(window_attention_kernel)");
+    built.store(regs = a.numRegs);
+  }
+  if (regs * W_THREADS < 128 * 88 + 256 * 208)
+    return fail(SI_ERR_CUDA, "window_attention_kernel was built with %d registers a thread", regs);
   return launch_tiles(window_attention_kernel<D, HALF, KT>, smem, p, D, HALF, KT, W_FEW, n_sm, stream);
 }
 

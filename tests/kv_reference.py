@@ -6,7 +6,7 @@ cache attention the query as two or three e4m3 terms whose absolute floor is
 2^-18 of the row's largest magnitude: |ds| <= 2^-16 * T with T = scale *
 max|q| * sum|k|, the largest over the visible keys.  Weights: rounded before
 the value product with a relative error of at most `step` (half a step of the
-type, 2^-9 bf16, 2^-12 fp16 twice over; two e4m3 terms: 2^-4 * 2^-4), so the
+type: 2^-8 bf16, 2^-11 fp16; two e4m3 terms: 2^-4 * 2^-4), so the
 numerator moves by at most (step + 2 |ds|) * W with W the weighted mean of |v|;
 below 2^-18 of the largest weight an absolute floor of 2^-19 of it applies to
 each of the n tokens, n * 2^-19 * max|v| / sum of weights, where the sum is at
