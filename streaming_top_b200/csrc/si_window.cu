@@ -838,7 +838,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = C->tmem_slot;
-  // items of this CTA, all with the same steps: number i waits for parity i & 1
+  // items of this CTA, all with the same steps (padding's too: skipping it cost
+  // the others 9 %, 197 against 180 us): number i waits for parity i & 1
 
   if (warp == 0) {
     if (lane == 0) {
@@ -848,9 +849,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       prefetch_tmap(&tm_v);
       uint32_t i = 0;
       bool v_began = false;
-      for (int n = blockIdx.x; n < p.items; n += gridDim.x) {
+      for (int n = blockIdx.x; n < p.items; n += gridDim.x, ++i) {
         const BandItem it = band_item(p, n);
-        if (it.p0 >= it.len) continue;  // padding alone
         if (!mbar_wait_bounded(&C->qk_empty, (i & 1u) ^ 1u, abort, limit)) {
           window_error(p, abort, WERR_Q);
           break;
@@ -873,7 +873,6 @@ __global__ void __launch_bounds__(W_THREADS, 1)
           tma_load_4d(v_s + c * plane + s16 * 128, &tm_v, &C->v_full, c * 64, it.h, it.k_start, it.b);
         }
         v_began = true;
-        ++i;
       }
       // every copy issued has landed before the CTA can exit
       bool ok = !i || mbar_wait_timed(&C->qk_full, (i - 1) & 1u, limit);
@@ -894,10 +893,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     };
     uint32_t i = 0;
     bool stop = false;
-    for (int n = blockIdx.x; n < p.items && !stop; n += gridDim.x) {
-      const BandItem it = band_item(p, n);
-      if (__all_sync(0xFFFFFFFFu, it.p0 >= it.len)) continue;
-      const uint32_t par = i++ & 1u;
+    for (int n = blockIdx.x; n < p.items && !stop; n += gridDim.x, ++i) {
+      const uint32_t par = i & 1u;
       if (!await(&C->qk_full, par, WERR_Q)) break;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
@@ -939,9 +936,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     // ------------------------------------------------------------ value check
     constexpr uint32_t EXP = HALF ? 0x7C007C00u : 0x7F807F80u, CARRY = HALF ? 0x04000400u : 0x00800080u;
     uint32_t i = 0;
-    for (int n = blockIdx.x; n < p.items; n += gridDim.x) {
+    for (int n = blockIdx.x; n < p.items; n += gridDim.x, ++i) {
       const BandItem it = band_item(p, n);
-      if (it.p0 >= it.len) continue;
       const int last = min(it.p0 + 2 * p.P, it.len) - 1;
       // the last item's verdict has been read, this one's values are here
       const bool got = mbar_wait_bounded(&C->checked, (i & 1u) ^ 1u, abort, limit) &&
@@ -973,7 +969,6 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // cleared values are read by the MMA
       __syncwarp();
       if (lane == 0) mbar_arrive(&C->v_ok);
-      ++i;
     }
   } else {
     // ------------------------------------------------------------ softmax and epilogue of a query tile
@@ -985,17 +980,9 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     uint8_t* stage = o_s + (warp - 4) * BAND_STAGE;
     const int chunks = (keys + 63) / 64;
     uint32_t i = 0;
-    for (int n = blockIdx.x; n < p.items; n += gridDim.x) {
+    for (int n = blockIdx.x; n < p.items; n += gridDim.x, ++i) {
       const BandItem it = band_item(p, n);
       const int pos = it.p0 + m * p.P + i_pos;
-      if (it.p0 >= it.len) {
-        if (used && pos < p.S) {
-          const size_t at = (static_cast<size_t>(it.b) * p.S + pos) * p.H + it.h * p.G + head_of;
-          for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(p.out + at * (D * 2) + c * 16) = make_uint4(0, 0, 0, 0);
-          if (p.lse) p.lse[at] = ninf;
-        }
-        continue;
-      }
       const uint32_t par = i & 1u;
       const bool live = used && pos < it.len;
       // seen: columns up to b that lie behind a, or before e; of the sinks' columns those before sink_end
@@ -1135,7 +1122,6 @@ __global__ void __launch_bounds__(W_THREADS, 1)
           if (rp < it.len) row_by_keys<D, HALF>(p, full, rp, it.h * p.G + r % p.G);
         }
       }
-      ++i;
     }
   }
 
