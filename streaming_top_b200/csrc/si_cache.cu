@@ -64,6 +64,26 @@ __device__ __forceinline__ float2 decode2(uint32_t codes) {
 
 constexpr int AP_VECS = 8;
 
+// The largest finite magnitude of a thread's own vectors, where they hold an
+// infinity or NaN.  A call: in line, 8 prompts of 2048 to 4096 tokens took 35 for 31 us.
+template <int D, bool HALF>
+__device__ __noinline__ uint32_t finite_top(const uint8_t* rows, int cnt, size_t stride) {
+  constexpr uint32_t LIMIT = HALF ? 0x7C00u : 0x7F80u;
+  constexpr int VROW = D / 8;
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int vec = threadIdx.x; vec / VROW < cnt; vec += blockDim.x) {
+    const uint4 y = *reinterpret_cast<const uint4*>(rows + (vec / VROW) * stride + (vec % VROW) * 16);
+    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo16 = w[i] & 0x7FFFu, hi16 = (w[i] >> 16) & 0x7FFFu;
+      top = max(top, max(lo16 < LIMIT ? lo16 : 0u, hi16 < LIMIT ? hi16 : 0u));
+    }
+  }
+  return top;
+}
+
 template <int D, bool HALF>
 __global__ void __launch_bounds__(256, 4) cache_append_kernel(const AppendParams p) {
   constexpr int VROW = D / 8;  // 16-byte input vectors of a row
@@ -106,19 +126,8 @@ __global__ void __launch_bounds__(256, 4) cache_append_kernel(const AppendParams
     top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[j].x & 0x7FFF7FFFu, x[j].y & 0x7FFF7FFFu),
                                  __vmaxu2(x[j].z & 0x7FFF7FFFu, x[j].w & 0x7FFF7FFFu)));
   top = max(top & 0xFFFFu, top >> 16);
-  if (top >= LIMIT) {  // not finite: once more, without those
-    top = 0;
-#pragma unroll 1
-    for (int i = threadIdx.x; i < cnt * D / 2; i += blockDim.x) {
-      // the thread's own vectors, word by word
-      const int vec = threadIdx.x + (i / static_cast<int>(blockDim.x) / 4) * blockDim.x, row = vec / VROW;
-      if (row >= cnt) break;
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(rows + static_cast<size_t>(row) * p.H_kv * (D * 2) + (vec % VROW) * 16 +
-                                                            (i / static_cast<int>(blockDim.x) % 4) * 4);
-      const uint32_t lo16 = w & 0x7FFFu, hi16 = (w >> 16) & 0x7FFFu;
-      top = max(top, max(lo16 < LIMIT ? lo16 : 0u, hi16 < LIMIT ? hi16 : 0u));
-    }
-  }
+  if (top >= LIMIT)  // not finite
+    top = finite_top<D, HALF>(rows, cnt, static_cast<size_t>(p.H_kv) * (D * 2));
   const float amax = to_float2<HALF>(top).x;
   const uint32_t wm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax));  // non-negative: bits order as values
   if ((threadIdx.x & 31) == 0) s_amax[threadIdx.x >> 5] = wm;
