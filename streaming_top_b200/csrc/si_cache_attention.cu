@@ -630,8 +630,9 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
             if (sub == 0) {
               const long long pos = len - p.L + row_i[j];
               const int ps = static_cast<int>(pos < 0 ? -1 : pos);
-              // e4m3 has no infinity: a row that holds one scores NaN
-              C->qs[qb][r] = amax <= 3.402823466e38f ? sc * p.scale_log2 : __int_as_float(0x7fc00000);
+              // e4m3 has no infinity: a row that holds one scores NaN.  Never 0 (the
+              // least float stands for less): a masked score is -inf times this.
+              C->qs[qb][r] = amax <= 3.402823466e38f ? fmaxf(sc * p.scale_log2, __int_as_float(1)) : __int_as_float(0x7fc00000);
               C->pos[qb][r] = ps;
               C->low[qb][r] = p.window && p.window <= ps ? ps - p.window : -1;
               C->out[qb][r] = out_at[j];

@@ -8,6 +8,8 @@ from tests.test_gpu_cache import _cuda, _gen, _i32, _run_append
 
 pytestmark = pytest.mark.gpu
 
+import streaming_top_b200 as si  # noqa: E402
+
 
 # ------------------------------------------------------------------ append
 
@@ -52,3 +54,31 @@ def test_append_step_that_is_not_finite(page):
         k[b, 0, :, 41 + b] = 50.0 * 2.0 ** b
     _run_append(pool, k.bfloat16(), -k.half().bfloat16(), torch.arange(B, dtype=torch.int32)[:, None],
                 _i32([page - 1 - b for b in range(B)]), None)
+
+
+# ------------------------------------------------------------------ attention over the cache
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("scale", [0.0, 1e-10, 1e-38])
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (30, 3)])
+def test_cache_attention_of_queries_that_are_zero(dtype, scale, window, n_sink):
+    """Queries of zeros, or nearly, at any score scale: the mean of what they see, ln of its count."""
+    g = _gen(50)
+    page, D, lens = 16, 64, [200, 77]
+    kp, vp = [torch.randint(0x30, 0x71, (30, 1, page, D), generator=g, dtype=torch.int16).to(torch.uint8) for _ in range(2)]
+    ks = vs = torch.full((30, 1), 2.0 ** -7)
+    table = torch.randperm(30, generator=g).int().view(2, 15)
+    q = torch.zeros((2, 2, 8, D), dtype=dtype)
+    q[:, :, 1::2] = torch.finfo(dtype).tiny if scale else 0
+    out, lse = si.cache_attention(q.cuda(), si.PagedCache(*_cuda(kp, vp, ks, vs)), table.cuda(), _i32(lens).cuda(),
+                                  scale=scale, window=window, n_sink=n_sink)
+    for b, n in enumerate(lens):
+        v = vp[table[b].long()].view(torch.float8_e4m3fn).double().reshape(-1, D) * 2.0 ** -7
+        for i in range(2):
+            p = n - 2 + i
+            see = [j for j in range(p + 1) if not window or j > p - window or j < n_sink]
+            # a weight (equal ones: 256, exact in every form) and fp32 sums, then one rounding of the output
+            half = torch.finfo(dtype).eps / 2
+            assert torch.allclose(out[b, i].cpu().double(), v[see].mean(0).expand(8, D), rtol=half + 2.0 ** -18, atol=0)
+            assert torch.allclose(lse[b, i].cpu().double(), torch.tensor(float(len(see))).double().log(), rtol=2.0 ** -20)
