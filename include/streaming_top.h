@@ -342,7 +342,10 @@ SI_API si_status si_cache_append(const si_cache* cache, const void* k, const voi
  * among them) gets out = 0 and lse = -inf.  Tokens of pages that are missing
  * (entries outside [0, n_pages)) are not visible; lens[b] beyond max_pages *
  * page is read as that.  What lies in slots that nobody sees (NaN, stale
- * codes) has no effect.  scale 0 = 1/sqrt(D).  dtype SI_DTYPE_BF16 or
+ * codes) has no effect.  Sums are fp32.  The softmax weights are rounded to 8
+ * bits before the value product (fp16: to 11); within 128 tokens, those whose
+ * weight times their page's value scale lies below 2^-14 of the largest such
+ * product are off by 2^-21 of it at most (fp16: 2^-25).  scale 0 = 1/sqrt(D).  dtype SI_DTYPE_BF16 or
  * SI_DTYPE_FP16.  H a multiple of H_kv, H / H_kv <= 128; L >= 1; window and
  * n_sink >= 0.  Scratch for partial results is taken from opt->workspace when
  * it is given and large enough (si_cache_attention_workspace_size()), else

@@ -11,16 +11,21 @@
 // lanes and the few query rows on N, so no lane of the tensor core's M is
 // padding.  q and the softmax weights, which have more bits than e4m3, enter
 // as sums of e4m3 terms (two carry 8 bits, bf16's own precision; three the 11
-// of fp16): q = 2^x (t0 + t1 [+ t2]), each term the rounded rest.  The terms
-// stand side by side on N, so that the cached tile, whose reading bounds a
+// of fp16): q = 2^x (t0 + t1 / 16 [+ t2 / 256]), each term the rounded rest.  The
+// terms stand side by side on N, so that the cached tile, whose reading bounds a
 // product with so few columns, is read once for all of them, and their
-// columns are added up when the accumulator is read.  With x
-// from the row's largest magnitude (224 .. 448) bf16's terms are exact down to
-// 2^-14 of it, then off by 2^-19 of it at most.  P is scaled likewise: a
-// tile's weights are taken relative to the tile's own maximum and to its
-// largest value scale, P = 256 exp2(s - m_tile) v_scale / v_ref, so that a tile
-// far below the running maximum keeps its precision, and the value scales cost
-// nothing.  The running state joins tiles as usual, in fp32.
+// columns are added up when the accumulator is read.  With x from the row's
+// largest magnitude (224 .. 448) bf16's terms are exact down to 2^-13 of it, then
+// off by 2^-21 of it at most (fp16: 2^-14, 2^-25).
+//
+// P carries the value scales: P = 256 exp2(s - m) v_scale / v_ref, where m is the
+// largest of s + log2(v_scale / v_ref) over what the row sees of the tile (with
+// the scale's power of two; v_ref the tile's largest scale).  So P is 128 or more
+// where weight times scale is largest, whichever of the two makes it so, and a
+// tile far below the running maximum keeps its precision.  A weight is rounded by
+// 2^-8 of itself (fp16: 2^-11), where weight times scale is below 2^-14 of the
+// tile's largest by 2^-21 of that at most (fp16: 2^-25).  The sum takes the
+// weights themselves, unrounded, and the running state joins tiles as usual; both in fp32.
 //
 // Work: tiles of 128 tokens.  All CTAs get equal runs of consecutive tiles of
 // the whole batch (sequence, head, rows, tile), whatever its lengths; a unit
@@ -53,6 +58,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -70,6 +76,7 @@ constexpr int C_ND = 8;          // tile descriptors in flight
 // tokens (16 tiles) 21.5 and 27.
 constexpr int C_WHOLE = 8;
 constexpr int C_MAX_CTAS = 512;  // of a launch
+constexpr int C_FAR = 80;  // value scales of a tile further apart than 2^C_FAR count as that far
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 enum { CERR_SLOT = 41, CERR_DESC = 42, CERR_FULL = 43, CERR_Q = 44, CERR_S = 45, CERR_P = 46, CERR_O = 47,
@@ -101,7 +108,8 @@ struct TileDesc {
   int left;             // the unit's tiles behind this one
   float vref;
   int tok[8];           // a page's first token
-  float ks[8], rv[8];   // its key scale, and value scale / v_ref * 256
+  float ks[8];          // its key scale
+  float rv[8], lr[8];   // value scale / v_ref = 2^lr rv / 256, rv in (128, 256]
 };
 
 // The visible pages of a sequence: sink_pages from 0 on, then those from `first`
@@ -192,16 +200,20 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
-// v[0..3] -= the values of four codes.
+// Term i of a sum of e4m3 terms is stored times TERM_UP^i: what a term leaves is
+// at most 1/16 of it, and so keeps off the codes' subnormal numbers for longer.
+constexpr float TERM_UP = 16.f;
+
+// What four codes leave of v[0..3], for the next term.
 __device__ __forceinline__ void take_off(float (&v)[4], uint32_t codes) {
   const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xFFFFu), __NV_E4M3);
   const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes >> 16), __NV_E4M3);
   const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
   const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
-  v[0] -= fa.x;
-  v[1] -= fa.y;
-  v[2] -= fb.x;
-  v[3] -= fb.y;
+  v[0] = (v[0] - fa.x) * TERM_UP;
+  v[1] = (v[1] - fa.y) * TERM_UP;
+  v[2] = (v[2] - fb.x) * TERM_UP;
+  v[3] = (v[3] - fb.y) * TERM_UP;
 }
 
 // Sizes of an instantiation: R query rows of a unit (8, 16, 32 or 64).
@@ -216,6 +228,11 @@ struct CacheShape {
   static constexpr int WG = R >= 32 ? 4 : 2;
   static constexpr int HC = R / WG;            // rows of a thread
   static constexpr int THREADS = 128 + 128 * WG;
+  // With sixteen rows a thread the softmax warps take registers from the others
+  // (96 a thread spill in the tile loop: 86 for 77 us with 262,143 tokens).
+  static constexpr bool SPLIT = HC > 8;
+  static constexpr int REGS_FEW = 64, REGS_MANY = 104, REGS = 96;
+  static_assert(!SPLIT || 128 * REGS_FEW + 128 * WG * REGS_MANY <= THREADS * REGS, "registers of a launch");
   static constexpr int SLOT = C_TILE * D;      // a K or V tile
   static constexpr int Q = N * D;              // one q buffer
   static constexpr int P = N * C_TILE;         // one P buffer
@@ -239,7 +256,7 @@ struct CacheCtrl {
   alignas(16) float red[2][R][4];     // per row and quadrant of lanes: the tile's maximum
   alignas(16) float sum[R][4];        // the same: the unit's sum
   alignas(16) float2 ab[2][R];        // per row: factors of the state and of the tile's O
-  alignas(16) float4 col[4 * Sh::WG][Sh::HC];   // per warp and row: score scale, the tile's maximum, factors of the state and of the tile
+  alignas(16) float4 col[4 * Sh::WG][Sh::HC];   // per warp and row: the tile's maximum, factors of the state and of the tile
   uint16_t nan_bits[2][C_TILE][D / 16];  // dims whose value is NaN, for tokens that only some rows see
   int nan_tok[2][8], nan_tile[2];     // first tokens of such a tile's pages, and its number
   long long scan[Sh::THREADS / 32];
@@ -371,6 +388,10 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
     }
   }
 
+  if constexpr (Sh::SPLIT) {
+    if (warp < 4) regs_dec<Sh::REGS_FEW>();
+    else regs_inc<Sh::REGS_MANY>();
+  }
   if (warp == 0) {
     // ------------------------------------------------------------ scheduler and TMA
     const int npg = C_TILE / p.page, group = 32 / npg;  // pages of a tile; tiles that the warp looks up at once
@@ -404,7 +425,12 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
                                                        static_cast<long long>(tok) + p.page <= p.n_sink));
       float vref = vs;
       for (int o = npg >> 1; o; o >>= 1) vref = fmaxf(vref, __shfl_xor_sync(0xFFFFFFFFu, vref, o));
-      const float rv = vref > 0.f ? vs / vref * 256.f : 0.f;
+      // the scale's power of two goes into the scores, the rest into the weights
+      float rv = vref > 0.f ? vs / vref * 256.f : 0.f;
+      const uint32_t rv_bits = __float_as_uint(rv);
+      const int e = max(static_cast<int>(rv_bits >> 23) - 135 + ((rv_bits & 0x7FFFFFu) != 0), -C_FAR);
+      const float lr = static_cast<float>(e);
+      rv *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       for (int i = 0; i < cnt; ++i, ++t) {
         const int ds = static_cast<int>(t % C_ND);
         if (!mbar_wait_bounded(&C->d_empty[ds], (static_cast<uint32_t>(t / C_ND) & 1u) ^ 1u, abort, limit)) {
@@ -422,6 +448,7 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
           d.tok[pj] = tok;
           d.ks[pj] = ks;
           d.rv[pj] = rv;
+          d.lr[pj] = lr;
           if (pj == 0) {
             const uint32_t pages = (there_bits >> (gi * npg)) & ((1u << npg) - 1u);
             const bool every = pages == (1u << npg) - 1u && ((clear_bits >> (gi * npg)) & ((1u << npg) - 1u)) == (1u << npg) - 1u;
@@ -571,7 +598,7 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
       ++n_unit;
       const long long len = p.lens[b];
       // eight lanes a row, four rows at a time, the loads of several steps under way together
-      constexpr int EL = D / 8, STEPS = R / 8 < 4 ? R / 8 : 4;  // a lane's dims
+      constexpr int EL = D / 8, STEPS = R / 8 < 2 ? 1 : R == 32 ? 4 : 2;  // a lane's dims
       const int sub = lane & 7;
 #pragma unroll 1
       for (int r0 = (warp - 2) * 4 + (lane >> 3); r0 - (lane >> 3) < rows; r0 += 8 * STEPS) {
@@ -630,9 +657,8 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
             if (sub == 0) {
               const long long pos = len - p.L + row_i[j];
               const int ps = static_cast<int>(pos < 0 ? -1 : pos);
-              // e4m3 has no infinity: a row that holds one scores NaN.  Never 0 (the
-              // least float stands for less): a masked score is -inf times this.
-              C->qs[qb][r] = amax <= 3.402823466e38f ? fmaxf(sc * p.scale_log2, __int_as_float(1)) : __int_as_float(0x7fc00000);
+              // e4m3 has no infinity: a row that holds one scores NaN
+              C->qs[qb][r] = amax <= 3.402823466e38f ? sc * p.scale_log2 : __int_as_float(0x7fc00000);
               C->pos[qb][r] = ps;
               C->low[qb][r] = p.window && p.window <= ps ? ps - p.window : -1;
               C->out[qb][r] = out_at[j];
@@ -678,7 +704,7 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
 #pragma unroll
       for (int i = 1; i < TERMS; ++i)
 #pragma unroll
-        for (int c = 0; c < HC; ++c) v[c] += t[i - 1][c];
+        for (int c = 0; c < HC; ++c) v[c] = fmaf(t[i - 1][c], i == 1 ? 1.f / TERM_UP : 1.f / (TERM_UP * TERM_UP), v[c]);
     };
     // joins tile j's O into the state
     auto join = [&](long long j, int qb) -> bool {
@@ -720,7 +746,7 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
       }
       const TileDesc& d = C->desc[ds];
       const int flags = d.flags, tok = d.tok[page_of] + me % p.page;
-      const float ks = d.ks[page_of], rv = d.rv[page_of], vref = d.vref;
+      const float ks = d.ks[page_of], rv = d.rv[page_of], lr = d.lr[page_of], vref = d.vref;
       if (flags & F_FIRST) {
         ++n_unit;
         got = mbar_wait_bounded(&C->q_full[(n_unit - 1) & 1], ((n_unit - 1) >> 1) & 1u, abort, limit);
@@ -745,9 +771,9 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
       tc_fence_after();
       float s[HC];
       load_terms(tmem + lanes + sb * N + c0, s);
-      // (a row's own scale is positive: it can follow the maximum)
+      // log2 of weight times value scale, before the mask: a row's own scale may be 0
 #pragma unroll
-      for (int c = 0; c < HC; ++c) s[c] *= ks;
+      for (int c = 0; c < HC; ++c) s[c] = fmaf(s[c] * ks, C->qs[qb][c0 + c], lr);
       if (flags & F_MASK) {
         const bool there = (d.pages >> page_of) & 1;
 #pragma unroll
@@ -765,15 +791,16 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
       // a lane a row: the tile's maximum, the state's factor and the tile's (one of them is 1)
       if (lane < HC) {
         const float4 r = *reinterpret_cast<const float4*>(C->red[sb][c0 + lane]);
-        const float q = C->qs[qb][c0 + lane], mt = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)) * q;
+        const float mt = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w));
         const float f = mt == m ? 1.f : ex2(-fabsf(m - mt));
         const bool up = mt > m;
         const float fa = up ? f : 1.f, fb = up ? 1.f : f;
         m = fmaxf(m, mt);
-        col[lane] = make_float4(q, mt == ninf ? 0.f : mt, fa, fb);
+        col[lane] = make_float4(mt == ninf ? 0.f : mt, fa, fb, 0.f);
         if (quad == 0) C->ab[sb][c0 + lane] = make_float2(fa, fb * vref * (1.f / 256.f));
       }
       __syncwarp();
+      const float ilr = __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(lr)) << 23);  // 2^-lr: the sum is of weights alone
       // P in half precision (11 bits), then its terms, the row of a token
       // contiguous along N in groups of 16
 #pragma unroll
@@ -782,8 +809,8 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 k = col[c + i];
-          const float e = ex2(fmaf(s[c + i], k.x, -k.y));
-          l[c + i] = fmaf(e, k.w, l[c + i] * k.z);
+          const float e = ex2(s[c + i] - k.x);
+          l[c + i] = fmaf(e * ilr, k.z, l[c + i] * k.y);
           v[i] = e * rv;
         }
         __half2 x = __floats2half2_rn(v[0], v[1]), y = __floats2half2_rn(v[2], v[3]);
@@ -794,8 +821,9 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
           const int at = term * R + c0 + c;
           *reinterpret_cast<uint32_t*>(p_s + sb * Sh::P + (at >> 4) * 2048 + me * 16 + (at & 15)) = qx | (qy << 16);
           if (term + 1 < TERMS) {
-            x = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(qx), __NV_E4M3)));
-            y = __hsub2(y, __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(qy), __NV_E4M3)));
+            const __half2 up = __float2half2_rn(TERM_UP), dn = __float2half2_rn(-TERM_UP);  // exact: what is left has fewer bits
+            x = __hfma2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(qx), __NV_E4M3)), dn, __hmul2(x, up));
+            y = __hfma2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(qy), __NV_E4M3)), dn, __hmul2(y, up));
           }
         }
       }
@@ -981,6 +1009,19 @@ si_status launch_cache(CacheParams& p, const si_cache* c, int n_sm, const si_opt
   si_status st = encode_tmap(&tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c->k_pages, dims, &stride, box, D);
   if (st == SI_OK) st = encode_tmap(&tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c->v_pages, dims, &stride, box, D);
   if (st != SI_OK) return st;
+  if constexpr (Sh::SPLIT) {
+    // the register split has to fit the registers of the launch, a property of
+    // the build: its warps would wait for the rest forever
+    static std::atomic<int> built{0};
+    int regs = built.load();
+    if (regs == 0) {
+      cudaFuncAttributes a;
+      const cudaError_t e = cudaFuncGetAttributes(&a, cache_attention_kernel<D, R, HALF>);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes(cache_attention_kernel)");
+      built.store(regs = a.numRegs);
+    }
+    if (regs < Sh::REGS) return fail(SI_ERR_CUDA, "cache_attention_kernel was built with %d registers a thread", regs);
+  }
   p.chunks = (p.L * p.G + R - 1) / R;
   // the tiles that a sequence can have at most
   long long pages = p.max_pages;

@@ -1,9 +1,10 @@
 """Edges of the K/V-cache and window attention calls on a GPU: values that are
 not finite, scales and lengths out of the ordinary, waits that run out, other
-streams."""
+streams.  Outputs of the attentions are held to the bounds of tests/kv_bounds.py."""
 import pytest
 import torch
 
+from tests import kv_bounds
 from tests.test_gpu_cache import _cuda, _gen, _i32, _run_append
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +83,85 @@ def test_cache_attention_of_queries_that_are_zero(dtype, scale, window, n_sink):
             half = torch.finfo(dtype).eps / 2
             assert torch.allclose(out[b, i].cpu().double(), v[see].mean(0).expand(8, D), rtol=half + 2.0 ** -18, atol=0)
             assert torch.allclose(lse[b, i].cpu().double(), torch.tensor(float(len(see))).double().log(), rtol=2.0 ** -20)
+
+
+def _cache(pool):
+    return si.PagedCache(*_cuda(*pool))
+
+
+def _check_cache(q, pool, table, lens, sharp=2.0 ** -4, **kw):
+    """cache_attention against the bounds; `sharp` as in kv_bounds.check."""
+    word = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out, lse = si.cache_attention(q.cuda(), _cache(pool), table.cuda(), lens.cuda(), device_status=word, **kw)
+    assert word.eq(0).all()
+    kv_bounds.check(out, lse, kv_bounds.cache_attention(q, *pool, table, lens, **kw), sharp)
+    return out, lse
+
+
+def _positive(n_pages, G, page, D, g):
+    """A pool with keys of every sign and positive values, whose sums do not cancel."""
+    k = torch.randint(0, 256, (n_pages, G, page, D), generator=g, dtype=torch.int16)
+    k = torch.where(k % 128 > 0x50, k - 0x38, k).to(torch.uint8)
+    v = torch.randint(0x30, 0x71, (n_pages, G, page, D), generator=g, dtype=torch.int16).to(torch.uint8)
+    return [k, v, torch.full((n_pages, G), 2.0 ** -4), torch.full((n_pages, G), 2.0 ** -7)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D,H,L", [(128, 4, 1), (64, 4, 2), (128, 64, 1), (64, 64, 1), (128, 20, 1)])
+@pytest.mark.parametrize("apart", [6, 10, 14, 18, 30, 60])
+def test_cache_attention_weight_on_a_page_of_small_values(dtype, D, H, L, apart):
+    """All the weight lies on one page whose value scale is 2^-apart of its
+    neighbours': its values come out as exactly as any."""
+    g = _gen(apart)
+    page, n = 16, 300
+    n_pages = -(-n // page)
+    pool = _positive(n_pages, 1, page, D, g)
+    table = torch.randperm(n_pages, generator=g).int()[None]
+    for j in (2, 7, 9, 17):  # in the first tile, at its end, in the second, in the last
+        k, v, ks, vs = [t.clone() for t in pool]
+        k &= 0x8F  # small beside the first dim
+        p = int(table[0, j])
+        k[..., 0] = 0xB8  # -1
+        k[p, :, :, 0] = 0x38  # 1
+        vs[:] = 2.0 ** (apart - 3)
+        vs[p] = 2.0 ** -3
+        q = torch.randn((1, L, H, D), generator=g) * 0.1
+        q[..., 0] = (0.7 * (apart + 30)) * D ** 0.5 / 2 / 2.0 ** -4  # a score difference of 0.7 (apart + 30)
+        _check_cache(q.to(dtype), (k, v, ks, vs), table, _i32([n]))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("H", [4, 64])
+def test_cache_attention_beside_a_page_of_large_scale(dtype, window, H):
+    """Pages whose scale is 2^10 of the others': their visible values are zeros
+    (what made the scale large lies before the window), the others' count."""
+    g = _gen(window + H)
+    page, n, D = 16, 200, 128
+    n_pages = -(-n // page)
+    pool = _positive(n_pages, 1, page, D, g)
+    table = torch.randperm(n_pages, generator=g).int()[None]
+    for j in (3, (n - 70) // page):
+        p = int(table[0, j])
+        pool[3][p] *= 2.0 ** 10
+        pool[1][p, :, (n - 70) % page if window else 0:] = 0
+    q = (torch.randn((1, 1, H, D), generator=g) * 0.3).to(dtype)
+    _check_cache(q, pool, table, _i32([n]), window=window)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_cache_attention_weight_on_zeros(dtype):
+    """A page of scale zero takes nearly all the weight; the small rest is the output, and lse counts both."""
+    g = _gen(51)
+    pool = _positive(10, 1, 16, 128, g)
+    table = torch.arange(10, dtype=torch.int32)[None]
+    pool[0] &= 0x8F
+    pool[0][..., 0] = 0xB8
+    pool[0][4, :, :, 0] = 0x38
+    pool[3][4] = 0.0
+    q = torch.randn((1, 1, 8, 128), generator=g) * 0.1
+    q[..., 0] = 4.0 * 128 ** 0.5 / 2 / 2.0 ** -4  # a score difference of 4
+    _check_cache(q.to(dtype), pool, table, _i32([150]))
+    pool[3][:] = 0.0
+    out, _ = si.cache_attention(q.to(dtype).cuda(), _cache(pool), table.cuda(), _i32([150]).cuda())
+    assert (out == 0).all()
