@@ -165,3 +165,35 @@ def test_cache_attention_weight_on_zeros(dtype):
     pool[3][:] = 0.0
     out, _ = si.cache_attention(q.to(dtype).cuda(), _cache(pool), table.cuda(), _i32([150]).cuda())
     assert (out == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("H,L", [(2, 1), (16, 1), (64, 1), (12, 3)])
+def test_cache_attention_of_a_long_context_to_its_bounds(dtype, H, L):
+    """Sequences of tens of thousands of tokens, cut between blocks and joined,
+    some pages with much larger values than others: a lost part would show."""
+    g = _gen(H)
+    lens, page, D = [40000, 13, 4000], 64, 128
+    need = [-(-n // page) for n in lens]
+    pool = _positive(sum(need), 1, page, D, g)
+    pool[3] = torch.exp2(torch.randint(-9, -5, (sum(need), 1), generator=g).float()) * (
+        1 + torch.rand((sum(need), 1), generator=g))
+    order = torch.randperm(sum(need), generator=g).int()
+    pool[3][order[::20].long()] *= 16
+    table = torch.full((3, max(need)), -1, dtype=torch.int32)
+    for b, part in enumerate(order.split(need)):
+        table[b, : need[b]] = part
+    q = (torch.randn((3, L, H, D), generator=g) * 0.5).to(dtype)
+    _check_cache(q, pool, table, _i32(lens))
+    _check_cache(q, pool, table, _i32(lens), window=3000, n_sink=40)
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 5])
+def test_cache_attention_of_few_tokens_has_all_its_bits(n):
+    """fp16 keeps its 11 bits, bf16 its 8: of few tokens, whose roundings do not average out."""
+    for dtype in (torch.bfloat16, torch.float16):
+        g = _gen(n)
+        pool = _positive(40, 4, 16, 128, g)
+        table = torch.arange(40, dtype=torch.int32)[:, None]
+        q = (torch.randn((40, 1, 64, 128), generator=g) * 0.5).to(dtype)
+        _check_cache(q, pool, table, _i32([n] * 40))
