@@ -341,7 +341,7 @@ SI_API si_status si_cache_append(const si_cache* cache, const void* k, const voi
  * over the visible tokens.  A query that sees nothing (a negative position
  * among them) gets out = 0 and lse = -inf.  Tokens of pages that are missing
  * (entries outside [0, n_pages)) are not visible; lens[b] beyond max_pages *
- * page is read as that.  What lies in slots that nobody sees (NaN, stale
+ * page is read as that: the queries are then the table's last tokens.  What lies in slots that nobody sees (NaN, stale
  * codes) has no effect.  Sums are fp32.  The softmax weights are rounded to 8
  * bits before the value product (fp16: to 11); within 128 tokens, those whose
  * weight times their page's value scale lies below 2^-14 of the largest such

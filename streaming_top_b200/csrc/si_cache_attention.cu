@@ -120,12 +120,17 @@ struct Span {
   int p_lo, p_hi;
 };
 
+// Tokens of a sequence: what lies beyond its row of the table is not there.
+__device__ __forceinline__ long long tokens_of(const CacheParams& p, int b) {
+  return min(static_cast<long long>(p.lens[b]), static_cast<long long>(p.max_pages) * p.page);
+}
+
 __device__ __forceinline__ Span span_of(const CacheParams& p, int b) {
   Span s;
-  const long long len = p.lens[b], cap = static_cast<long long>(p.max_pages) * p.page;
+  const long long len = tokens_of(p, b);
   const long long p_lo = len - p.L, p_hi = len - 1;
   // visible tokens: [0, sink) and [lo, hi)
-  const long long hi = max(min(p_hi + 1, cap), 0ll);
+  const long long hi = max(len, 0ll);
   const long long lo = p.window ? min(max(p_lo - p.window + 1, 0ll), hi) : 0;
   const long long sink = p.window ? min(static_cast<long long>(p.n_sink), hi) : 0;
   s.first = static_cast<int>(lo / p.page);
@@ -596,7 +601,7 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
         break;
       }
       ++n_unit;
-      const long long len = p.lens[b];
+      const long long len = tokens_of(p, b);
       // eight lanes a row, four rows at a time, the loads of several steps under way together
       constexpr int EL = D / 8, STEPS = R / 8 < 2 ? 1 : R == 32 ? 4 : 2;  // a lane's dims
       const int sub = lane & 7;

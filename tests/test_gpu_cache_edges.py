@@ -197,3 +197,15 @@ def test_cache_attention_of_few_tokens_has_all_its_bits(n):
         table = torch.arange(40, dtype=torch.int32)[:, None]
         q = (torch.randn((40, 1, 64, 128), generator=g) * 0.5).to(dtype)
         _check_cache(q, pool, table, _i32([n] * 40))
+
+
+@pytest.mark.parametrize("L,window,n_sink", [(1, 10, 0), (3, 10, 2), (2, 1, 0), (1, 0, 0), (4, 40, 5)])
+def test_cache_attention_length_beyond_the_table_is_the_tables(L, window, n_sink):
+    """A length beyond max_pages * page is read as that: the queries are the table's last tokens."""
+    g = _gen(52)
+    page, width = 16, 3
+    pool = _positive(12, 1, page, 64, g)
+    table = torch.randperm(12, generator=g).int().view(4, width)
+    q = (torch.randn((4, L, 4, 64), generator=g) * 0.5).bfloat16()
+    for lens in ([48, 49, 53, 1000], [2 ** 31 - 1, 48 + L, 47, 2 ** 31 - 49]):
+        _check_cache(q, pool, table, _i32(lens), window=window, n_sink=n_sink)
