@@ -1000,7 +1000,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       // One pass, 64 columns at a time: P relative to a whole power of two, taken
       // from the first columns that are seen; where a later column exceeds it by
       // more than 2^8, what was written is scaled, which a power of two does
-      // without rounding.
+      // without rounding (but where fp16 weights become subnormal: by 2^-25 at most).
       float ref = ninf;
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       const float2 sc = make_float2(p.scale_log2, p.scale_log2);
@@ -1033,6 +1033,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
           if (__any_sync(0xFFFFFFFFu, grow)) {
             const float to = ceilf(mt), f = grow ? ex2(ref - to) : 1.f;
             if (grow) ref = to;
+            tmem_st_wait();  // the weights of the columns before are there
 #pragma unroll
             for (int k = 0; k < 2; ++k) sum[k] = make_float2(sum[k].x * f, sum[k].y * f);
 #pragma unroll 1

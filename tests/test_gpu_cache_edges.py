@@ -209,3 +209,32 @@ def test_cache_attention_length_beyond_the_table_is_the_tables(L, window, n_sink
     q = (torch.randn((4, L, 4, 64), generator=g) * 0.5).bfloat16()
     for lens in ([48, 49, 53, 1000], [2 ** 31 - 1, 48 + L, 47, 2 ** 31 - 49]):
         _check_cache(q, pool, table, _i32(lens), window=window, n_sink=n_sink)
+
+
+# ------------------------------------------------------------------ prompts
+
+
+def _check_window(q, k, v, window, n_sink=0, lens=None, **kw):
+    word = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out, lse = si.window_attention(*_cuda(q, k, v), window=window, n_sink=n_sink,
+                                   lens=None if lens is None else lens.cuda(), device_status=word, **kw)
+    assert word.eq(0).all()
+    kv_bounds.check(out, lse, kv_bounds.window_attention(q, k, v, window, n_sink, lens, **kw))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window,n_sink", [(128, 0), (128, 4), (200, 0), (60, 100)])
+@pytest.mark.parametrize("steps", [1, 7, 30])
+def test_narrow_band_whose_scores_keep_growing(dtype, D, window, n_sink, steps):
+    """Scores that climb by `steps` (to the base 2) every 16 keys: the reference
+    moves in most column blocks, and the weights written before follow it."""
+    g = _gen(steps)
+    S, H = 600, 8
+    q = torch.randn((1, S, H, D), generator=g) * 0.05
+    k = torch.randn((1, S, 1, D), generator=g) * 0.05
+    v = torch.rand((1, S, 1, D), generator=g) + 0.1
+    q[..., 0] = 4.0
+    climb = steps / 16 * 0.6931 * D ** 0.5 / 4.0  # a key
+    k[0, :, 0, 0] = (torch.arange(S) - S / 2) * climb
+    _check_window(q.to(dtype), k.to(dtype), v.to(dtype), window, n_sink)
