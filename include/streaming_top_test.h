@@ -38,6 +38,16 @@ SI_API si_status si_test_stream_timeout(const void* q, const void* kc, const flo
  */
 SI_API void si_test_fail_allocations(int n);
 
+/*
+ * The same for the attention kernels of the raw-token branch: block 0 of the
+ * next n si_window_attention and si_cache_attention calls leaves out one load
+ * of keys, and every wait of these calls is limited to wait_limit_ns (1 ms at
+ * least).  The waits run out, the kernels record SI_ERR_TIMEOUT, drain the
+ * copies and products in flight and exit; outputs are unspecified.  n <= 0
+ * clears the hook.  Process-wide.
+ */
+SI_API void si_test_withhold_loads(int n, unsigned long long wait_limit_ns);
+
 #ifdef __cplusplus
 }
 #endif

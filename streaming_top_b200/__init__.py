@@ -105,6 +105,8 @@ _lib.si_version.restype = _i
 _lib.si_version.argtypes = []
 _lib.si_test_fail_allocations.restype = None
 _lib.si_test_fail_allocations.argtypes = [_i]
+_lib.si_test_withhold_loads.restype = None
+_lib.si_test_withhold_loads.argtypes = [_i, ctypes.c_ulonglong]
 _lib.si_test_stream_timeout.restype = _i
 _lib.si_test_stream_timeout.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, ctypes.c_ulonglong, _vp]
 
@@ -778,3 +780,9 @@ def test_fail_allocations(n: int) -> None:
     """Test hook: the library's next n scratch allocations fail as if the
     device were out of memory (``si_test_fail_allocations``)."""
     _lib.si_test_fail_allocations(int(n))
+
+
+def test_withhold_loads(n: int, wait_limit_ns: int = 50_000_000) -> None:
+    """Test hook: block 0 of the next n attention calls of the raw-token branch
+    leaves out a load and their waits are limited (``si_test_withhold_loads``)."""
+    _lib.si_test_withhold_loads(int(n), int(wait_limit_ns))

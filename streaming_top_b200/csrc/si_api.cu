@@ -23,6 +23,18 @@ __device__ int g_device_error[4];
 // Test hook: the next g_fail_allocs scratch allocations of the library fail.
 std::atomic<int> g_fail_allocs{0};
 
+// Test hook: the next g_withhold attention calls leave out a load.
+std::atomic<int> g_withhold{0};
+std::atomic<uint64_t> g_withhold_ns{0};
+
+// Takes one of the calls that a hook counts.
+bool take_one(std::atomic<int>& hook) {
+  int left = hook.load();
+  while (left > 0 && !hook.compare_exchange_weak(left, left - 1)) {
+  }
+  return left > 0;
+}
+
 // The library's stream-ordered memory pool per device.  Scratch that calls
 // allocate and free on their stream comes from it; it keeps up to
 // kPoolKeepBytes of freed memory between calls (the default pool would give
@@ -102,10 +114,7 @@ si_status error_word(const si_options* opt, int** out) {
 
 si_status scratch_alloc(void** p, size_t bytes, cudaStream_t stream, const char* what) {
   *p = nullptr;
-  int left = g_fail_allocs.load();
-  while (left > 0 && !g_fail_allocs.compare_exchange_weak(left, left - 1)) {
-  }
-  if (left > 0)
+  if (take_one(g_fail_allocs))
     return fail(SI_ERR_OUT_OF_MEMORY, "allocating %zu bytes for %s: failed by the allocation-failure test hook",
                 bytes, what);
   int dev = 0;
@@ -122,6 +131,12 @@ si_status scratch_alloc(void** p, size_t bytes, cudaStream_t stream, const char*
     if (e == cudaErrorMemoryAllocation) break;
   }
   return fail(SI_ERR_OUT_OF_MEMORY, "cudaMallocFromPoolAsync(%zu) for %s: %s", bytes, what, cudaGetErrorString(e));
+}
+
+bool take_withheld_load(uint64_t* limit_ns) {
+  if (!take_one(g_withhold)) return false;
+  *limit_ns = g_withhold_ns.load();
+  return true;
 }
 
 si_status encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base, const uint64_t* dims,
@@ -474,6 +489,11 @@ const char* si_status_string(si_status s) {
 const char* si_last_error(void) { return g_last_error; }
 
 void si_test_fail_allocations(int n) { g_fail_allocs.store(n > 0 ? n : 0); }
+
+void si_test_withhold_loads(int n, unsigned long long wait_limit_ns) {
+  g_withhold_ns.store(wait_limit_ns > 1000000ull ? wait_limit_ns : 1000000ull);
+  g_withhold.store(n > 0 ? n : 0);
+}
 
 int si_version(void) { return 300; }
 

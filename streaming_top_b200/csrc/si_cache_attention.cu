@@ -95,6 +95,7 @@ struct CacheParams {
   int* err;
   long long rows_total;  // rows of the pools
   int B, L, H, H_kv, G, page, max_pages, n_pages, window, n_sink, chunks, cut;
+  int withhold;  // test: block 0 leaves out the keys of its second tile
   float scale_log2;
   uint64_t wait_limit_ns;
 };
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
       rv *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       for (int i = 0; i < cnt; ++i, ++t) {
         const int ds = static_cast<int>(t % C_ND);
-        if (!mbar_wait_bounded(&C->d_empty[ds], (static_cast<uint32_t>(t / C_ND) & 1u) ^ 1u, abort, limit)) {
+        if (!mbar_wait_warp(&C->d_empty[ds], (static_cast<uint32_t>(t / C_ND) & 1u) ^ 1u, abort, limit)) {
           if (lane == 0) cache_error(p, abort, CERR_DESC);
           stop = true;
           break;
@@ -476,19 +477,21 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
         __syncwarp();
         if (lane == 0) mbar_arrive(&C->d_full[ds]);
         for (int kv = 0; kv < 2; ++kv) {
-          if (!mbar_wait_bounded(&C->empty[slot], phase ^ 1u, abort, limit)) {
+          if (!mbar_wait_warp(&C->empty[slot], phase ^ 1u, abort, limit)) {
             if (lane == 0) cache_error(p, abort, CERR_SLOT);
             stop = true;
             break;
           }
-          if (lane == 0) {
-            if (kv == 0) C->k_flags[slot] = d.flags;
-            mbar_arrive_expect_tx(&C->full[slot], Sh::SLOT);
+          if (!(p.withhold && blockIdx.x == 0 && t == 1 && kv == 0)) {
+            if (lane == 0) {
+              if (kv == 0) C->k_flags[slot] = d.flags;
+              mbar_arrive_expect_tx(&C->full[slot], Sh::SLOT);
+            }
+            __syncwarp();
+            if (gi == i) tma_load_2d(kv_s + slot * Sh::SLOT + pj * p.page * D, kv ? &tm_v : &tm_k, &C->full[slot], 0, y);
+            any |= 1u << slot;
+            last_par = (last_par & ~(1u << slot)) | (phase << slot);
           }
-          __syncwarp();
-          if (gi == i) tma_load_2d(kv_s + slot * Sh::SLOT + pj * p.page * D, kv ? &tm_v : &tm_k, &C->full[slot], 0, y);
-          any |= 1u << slot;
-          last_par = (last_par & ~(1u << slot)) | (phase << slot);
           if (++slot == NS) {
             slot = 0;
             phase ^= 1u;
@@ -586,7 +589,7 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
     uint32_t n_unit = 0;
     for (long long t = 0; t < n_tiles; ++t) {
       const int ds = static_cast<int>(t % C_ND);
-      if (!mbar_wait_bounded(&C->d_full[ds], static_cast<uint32_t>(t / C_ND) & 1u, abort, limit)) {
+      if (!mbar_wait_warp(&C->d_full[ds], static_cast<uint32_t>(t / C_ND) & 1u, abort, limit)) {
         if (lane == 0) cache_error(p, abort, CERR_DESC);
         break;
       }
@@ -596,7 +599,7 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
       if (lane == 0) mbar_arrive(&C->d_empty[ds]);
       if (!(flags & F_FIRST)) continue;
       const uint32_t qb = n_unit & 1;
-      if (!mbar_wait_bounded(&C->q_empty[qb], ((n_unit >> 1) & 1u) ^ 1u, abort, limit)) {
+      if (!mbar_wait_warp(&C->q_empty[qb], ((n_unit >> 1) & 1u) ^ 1u, abort, limit)) {
         if (lane == 0) cache_error(p, abort, CERR_Q);
         break;
       }
@@ -1142,6 +1145,7 @@ si_status si_cache_attention(const void* q, const si_cache* c, const int32_t* ta
   p.n_sink = n_sink;
   p.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(c->D))) * LOG2E;
   p.wait_limit_ns = kDefaultWaitLimitNs;
+  p.withhold = take_withheld_load(&p.wait_limit_ns);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool half = dtype == SI_DTYPE_FP16;
   if (c->D == 128) return half ? launch_cache_rows<128, true>(p, c, n_sm, opt, s) : launch_cache_rows<128, false>(p, c, n_sm, opt, s);

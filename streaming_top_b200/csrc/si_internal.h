@@ -36,6 +36,10 @@ si_status error_word(const si_options* opt, int** out);
 // the allocation-failure test hook says so.
 si_status scratch_alloc(void** p, size_t bytes, cudaStream_t stream, const char* what);
 
+// Whether a test asks this call to leave out a load; if so *limit_ns is the
+// wait limit it asks for.
+bool take_withheld_load(uint64_t* limit_ns);
+
 // TMA tensor-map encoder (driver entry point, resolved once).
 si_status encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                          uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,

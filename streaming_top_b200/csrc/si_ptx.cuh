@@ -78,6 +78,11 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// The same for a converged warp: all its lanes go on, or all give up.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort, limit_ns));
+}
+
 // Waits for the phase with the given parity, bounded by wall time only (for
 // draining copies or MMAs that are in flight, which must land before the
 // CTA releases their buffers).

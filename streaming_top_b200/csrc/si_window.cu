@@ -66,6 +66,7 @@ struct WindowParams {
   int B, S, H, H_kv, G, P;  // P positions a query tile
   int window, n_sink, blocks, wide_out, band_keys, band_sinks;
   int items;  // B * H_kv * blocks: no more than rows
+  int withhold;  // test: block 0 leaves out a load of its second item
   float scale_log2;
   uint64_t wait_limit_ns;
 };
@@ -375,12 +376,14 @@ __global__ void __launch_bounds__(W_THREADS, 1)
               stop = true;
               break;
             }
-            mbar_arrive_expect_tx(full, bytes);
-            const CUtensorMap* tm = kv ? (few ? &tm_v_few : &tm_v) : (few ? &tm_k_few : &tm_k);
-            for (int c = 0; c < Sh::HALVES; ++c)
-              tma_load_4d((kv ? v_s : k_s) + slot * Sh::TILE + c * (KT * 128), tm, full, c * 64, it.h, key0, it.b);
-            any |= 1u << (slot + 16 * kv);
-            last = (last & ~(1u << (slot + 16 * kv))) | (phase << (slot + 16 * kv));
+            if (!(p.withhold && blockIdx.x == 0 && n_it == 2 && u + kv == 0)) {
+              mbar_arrive_expect_tx(full, bytes);
+              const CUtensorMap* tm = kv ? (few ? &tm_v_few : &tm_v) : (few ? &tm_k_few : &tm_k);
+              for (int c = 0; c < Sh::HALVES; ++c)
+                tma_load_4d((kv ? v_s : k_s) + slot * Sh::TILE + c * (KT * 128), tm, full, c * 64, it.h, key0, it.b);
+              any |= 1u << (slot + 16 * kv);
+              last = (last & ~(1u << (slot + 16 * kv))) | (phase << (slot + 16 * kv));
+            }
             if (++slots[kv] == (kv ? NV : NK)) {
               slots[kv] = 0;
               phases[kv] ^= 1u;
@@ -511,12 +514,12 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       if (!it.tiles) continue;
       const int last = min(it.p0 + 2 * p.P, it.len) - 1;  // the item's last position
       // the rows of the item before the last one have been written: again[] is free
-      if (!mbar_wait_bounded(&C->rows_done[n_it & 1], ((n_it >> 1) & 1u) ^ 1u, abort, limit)) {
+      if (!mbar_wait_warp(&C->rows_done[n_it & 1], ((n_it >> 1) & 1u) ^ 1u, abort, limit)) {
         if (lane == 0) window_error(p, abort, WERR_SCAN);
         break;
       }
       for (int u = 0; u < it.tiles; ++u) {
-        if (!mbar_wait_bounded(&C->v_full[slot], phase, abort, limit)) {
+        if (!mbar_wait_warp(&C->v_full[slot], phase, abort, limit)) {
           if (lane == 0) window_error(p, abort, WERR_V);
           stop = true;
           break;
@@ -1251,6 +1254,7 @@ si_status si_window_attention(const void* q, const void* k, const void* v, const
   p.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(D))) * LOG2E;
   // (an item that is done again key by key holds up its CTA for some 10 us a key at most)
   p.wait_limit_ns = kDefaultWaitLimitNs + static_cast<uint64_t>(S) * 10000;
+  p.withhold = take_withheld_load(&p.wait_limit_ns);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool half = dtype == SI_DTYPE_FP16;
   if (D == 128) return half ? launch_window_tiles<128, true>(p, n_sm, s) : launch_window_tiles<128, false>(p, n_sm, s);

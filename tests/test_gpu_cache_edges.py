@@ -238,3 +238,49 @@ def test_narrow_band_whose_scores_keep_growing(dtype, D, window, n_sink, steps):
     climb = steps / 16 * 0.6931 * D ** 0.5 / 4.0  # a key
     k[0, :, 0, 0] = (torch.arange(S) - S / 2) * climb
     _check_window(q.to(dtype), k.to(dtype), v.to(dtype), window, n_sink)
+
+
+# ------------------------------------------------------------------ waits that run out
+
+
+def _runs_out(call):
+    """With a load withheld the call returns, its status word says so, and the next call is right."""
+    word = torch.zeros(2, dtype=torch.int32, device="cuda")
+    want = call(word)
+    assert word.eq(0).all()
+    si.test_withhold_loads(1)
+    try:
+        call(word)
+        torch.cuda.synchronize()
+    finally:
+        si.test_withhold_loads(0)
+    assert int(word[0]) == si.SI_ERR_TIMEOUT and int(word[1]) > 0
+    assert si.device_status() == si.SI_OK  # (the shared record was not touched)
+    word.zero_()
+    for a, b in zip(call(word), want):
+        assert torch.equal(a, b)
+    assert word.eq(0).all()
+
+
+@pytest.mark.parametrize("window,n_sink", [(300, 0), (300, 20), (500, 5)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_window_attention_wait_that_runs_out(window, n_sink, D):
+    """Key tiles of 64 and of 128, several items a block."""
+    g = _gen(60)
+    q, k, v = [torch.randn((1, 8192, n, D), generator=g).bfloat16().cuda() for n in (16, 2, 2)]
+    _runs_out(lambda word: si.window_attention(q, k, v, window=window, n_sink=n_sink, device_status=word))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,n,window", [(4, 6000, 0), (16, 6000, 0), (64, 6000, 0), (8, 900, 0), (64, 3000, 200)])
+def test_cache_attention_wait_that_runs_out(dtype, D, H, n, window):
+    """Units cut between blocks and whole ones, all numbers of rows."""
+    g = _gen(61)
+    page, B = 64, 40
+    width = -(-n // page)
+    cache = _cache(_positive(B * width, 1, page, D, g))
+    table = torch.randperm(B * width, generator=g).int().view(B, width).cuda()
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    q = (torch.randn((B, 1, H, D), generator=g) * 0.5).to(dtype).cuda()
+    _runs_out(lambda word: si.cache_attention(q, cache, table, lens, window=window, device_status=word))
