@@ -850,24 +850,25 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       prefetch_tmap(&tm_q);
       prefetch_tmap(&tm_k);
       prefetch_tmap(&tm_v);
-      uint32_t i = 0;
-      bool v_began = false;
+      uint32_t i = 0, n_qk = 0, n_v = 0;  // items; loads issued
       for (int n = blockIdx.x; n < p.items; n += gridDim.x, ++i) {
         const BandItem it = band_item(p, n);
         if (!mbar_wait_bounded(&C->qk_empty, (i & 1u) ^ 1u, abort, limit)) {
           window_error(p, abort, WERR_Q);
           break;
         }
-        mbar_arrive_expect_tx(&C->qk_full, 2 * p.P * p.G * D * 2 + keys * D * 2);
-        for (int c = 0; c < HALVES; ++c) {
-          for (int m = 0; m < 2; ++m)
-            tma_load_4d(q_s + m * QT + c * 16384, &tm_q, &C->qk_full, c * 64, it.h * p.G, it.p0 + m * p.P, it.b);
-          if (s16) tma_load_4d(k_s + c * plane, &tm_k_sink, &C->qk_full, c * 64, it.h, 0, it.b);
-          tma_load_4d(k_s + c * plane + s16 * 128, &tm_k, &C->qk_full, c * 64, it.h, it.k_start, it.b);
+        if (!(p.withhold && blockIdx.x == 0 && i == 1)) {
+          mbar_arrive_expect_tx(&C->qk_full, 2 * p.P * p.G * D * 2 + keys * D * 2);
+          for (int c = 0; c < HALVES; ++c) {
+            for (int m = 0; m < 2; ++m)
+              tma_load_4d(q_s + m * QT + c * 16384, &tm_q, &C->qk_full, c * 64, it.h * p.G, it.p0 + m * p.P, it.b);
+            if (s16) tma_load_4d(k_s + c * plane, &tm_k_sink, &C->qk_full, c * 64, it.h, 0, it.b);
+            tma_load_4d(k_s + c * plane + s16 * 128, &tm_k, &C->qk_full, c * 64, it.h, it.k_start, it.b);
+          }
+          ++n_qk;
         }
         if (!mbar_wait_bounded(&C->v_empty, (i & 1u) ^ 1u, abort, limit)) {
           window_error(p, abort, WERR_V);
-          ++i;
           break;
         }
         mbar_arrive_expect_tx(&C->v_full, keys * D * 2);
@@ -875,11 +876,11 @@ __global__ void __launch_bounds__(W_THREADS, 1)
           if (s16) tma_load_4d(v_s + c * plane, &tm_v_sink, &C->v_full, c * 64, it.h, 0, it.b);
           tma_load_4d(v_s + c * plane + s16 * 128, &tm_v, &C->v_full, c * 64, it.h, it.k_start, it.b);
         }
-        v_began = true;
+        ++n_v;
       }
-      // every copy issued has landed before the CTA can exit
-      bool ok = !i || mbar_wait_timed(&C->qk_full, (i - 1) & 1u, limit);
-      if (v_began && !*abort) ok = mbar_wait_timed(&C->v_full, (i - 1) & 1u, limit) && ok;
+      // every copy issued has landed before the CTA can exit, whatever ended the loop
+      bool ok = !n_qk || mbar_wait_timed(&C->qk_full, (n_qk - 1) & 1u, limit);
+      if (n_v) ok = mbar_wait_timed(&C->v_full, (n_v - 1) & 1u, limit) && ok;
       if (!ok) window_error(p, abort, WERR_DRAIN);
     }
   } else if (warp == 1) {

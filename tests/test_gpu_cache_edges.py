@@ -262,10 +262,10 @@ def _runs_out(call):
     assert word.eq(0).all()
 
 
-@pytest.mark.parametrize("window,n_sink", [(300, 0), (300, 20), (500, 5)])
+@pytest.mark.parametrize("window,n_sink", [(128, 0), (100, 4), (300, 0), (300, 20), (500, 5)])
 @pytest.mark.parametrize("D", [64, 128])
 def test_window_attention_wait_that_runs_out(window, n_sink, D):
-    """Key tiles of 64 and of 128, several items a block."""
+    """The narrow form, key tiles of 64 and of 128, several items a block."""
     g = _gen(60)
     q, k, v = [torch.randn((1, 8192, n, D), generator=g).bfloat16().cuda() for n in (16, 2, 2)]
     _runs_out(lambda word: si.window_attention(q, k, v, window=window, n_sink=n_sink, device_status=word))
