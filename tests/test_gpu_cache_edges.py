@@ -284,3 +284,21 @@ def test_cache_attention_wait_that_runs_out(dtype, D, H, n, window):
     lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
     q = (torch.randn((B, 1, H, D), generator=g) * 0.5).to(dtype).cuda()
     _runs_out(lambda word: si.cache_attention(q, cache, table, lens, window=window, device_status=word))
+
+
+def test_window_attention_key_by_key_over_a_long_prompt():
+    """A block that is done again key by key keeps its other warps waiting for seconds: the limits allow for it."""
+    g = _gen(62)
+    S, D = 600_000, 128
+    q, k, v = [torch.randn((1, S, 1, D), generator=g).bfloat16() for _ in range(3)]
+    v = v.abs() + 0.1
+    word = torch.zeros(2, dtype=torch.int32, device="cuda")
+    qd, kd, vd = _cuda(q, k, v)
+    vd[0, S - 5, 0, 3] = float("nan")
+    out, lse = si.window_attention(qd, kd, vd, window=S, device_status=word)
+    assert word.eq(0).all()
+    assert torch.isnan(out[0, S - 5:, 0, 3]).all() and torch.isnan(out).sum() == 5
+    pos = torch.tensor([S - 7, S - 250, S - 300])  # in that block, and before it
+    see = torch.arange(S) <= pos[:, None]
+    want = kv_bounds.attend(q[0, pos], k[0], v[0], see, D ** -0.5, *kv_bounds.WINDOW[torch.bfloat16], 2.0 ** -8)
+    kv_bounds.check(out[0, pos.cuda()], lse[0, pos.cuda()], want)
