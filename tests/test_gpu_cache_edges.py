@@ -302,3 +302,122 @@ def test_window_attention_key_by_key_over_a_long_prompt():
     see = torch.arange(S) <= pos[:, None]
     want = kv_bounds.attend(q[0, pos], k[0], v[0], see, D ** -0.5, *kv_bounds.WINDOW[torch.bfloat16], 2.0 ** -8)
     kv_bounds.check(out[0, pos.cuda()], lse[0, pos.cuda()], want)
+
+
+# ------------------------------------------------------------------ other streams
+
+
+def _attention_calls():
+    """{name: (a call on a stream, its inputs, where the outputs are)}, each tensor larger than the allocator's small blocks."""
+    def window():
+        x = [torch.randn((1, 8192, n, 64), device="cuda").bfloat16() for n in (16, 4, 4)]
+        return x, lambda s: si.window_attention(*x, window=100, stream=s)
+
+    def cache():
+        pool = [torch.zeros((512, 4, 64, 64), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        pool += [torch.ones((512, 4), device="cuda") for _ in range(2)]
+        q = torch.randn((512, 4, 16, 64), device="cuda").half()
+        table = torch.arange(512, dtype=torch.int32, device="cuda")[:, None].repeat(1, 2048).contiguous()
+        lens = torch.full((512,), 60, dtype=torch.int32, device="cuda")
+        x = [q, table, *pool]
+        return x, lambda s: si.cache_attention(q, si.PagedCache(*pool), table, lens, stream=s)
+
+    def top_k():
+        x = [torch.randn(shape, device="cuda").to(dt) for shape, dt in (
+            ((1, 4096, 64, 128), torch.bfloat16), ((1, 8192, 128), torch.bfloat16), ((1, 4096, 64), torch.float32))]
+        return x, lambda s: si.indexer_topk(*x, 4, 128, stream=s)
+
+    def sparse():
+        q = torch.randn((1, 256, 64, 576), device="cuda").bfloat16()
+        kv = torch.randn((1, 1024, 576), device="cuda").bfloat16()
+        idx = torch.randint(0, 1024, (1, 256, 128), dtype=torch.int32, device="cuda")
+        return [q, kv], lambda s: si.sparse_attention(q, kv, idx, stream=s)
+
+    return {"window": window, "cache": cache, "top-k": top_k, "sparse": sparse}
+
+
+def _busy(stream):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(400_000_000)  # some 0.2 s
+
+
+@pytest.mark.parametrize("name", list(_attention_calls()))
+def test_memory_of_a_call_on_another_stream_is_not_given_out(name):
+    """Inputs and outputs that the caller drops while the call waits on its
+    stream keep their memory, and a call's outputs do not take memory that work
+    of the current stream still uses."""
+    x, call = _attention_calls()[name]()
+    s = torch.cuda.Stream()
+    call(s)
+    torch.cuda.synchronize()
+    outs = call(s)
+    torch.cuda.synchronize()
+    sizes = [t.numel() * t.element_size() for t in (*x, *outs)]
+    del outs
+    torch.cuda.empty_cache()
+    _busy(s)
+    outs = call(s)
+    taken = {t.data_ptr() for t in (*x, *outs)}
+    x.clear()
+    del outs, call
+    new = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+    assert not s.query(), "the stream was to be busy still"
+    assert not taken & {t.data_ptr() for t in new}
+    torch.cuda.synchronize()
+    # the other way round: the current stream's own memory
+    del new
+    x, call = _attention_calls()[name]()
+    out_sizes = [t.numel() * t.element_size() for t in call(None)]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in out_sizes]
+    taken = {t.data_ptr() for t in held}
+    _busy(torch.cuda.current_stream())
+    del held
+    outs = call(s)
+    assert not torch.cuda.current_stream().query(), "the stream was to be busy still"
+    assert not taken & {t.data_ptr() for t in outs}
+    torch.cuda.synchronize()
+    for a, b in zip(outs, call(None)):
+        assert torch.equal(a, b)
+
+
+def test_captured_calls_on_a_side_stream():
+    """A step of append and attention on a side stream of a capture, over a
+    cache whose units are cut between blocks, and two such graphs replayed at once."""
+    g = _gen(70)
+    page, D, H, n = 64, 128, 16, 5000
+    width = -(-(n + 8) // page)
+    pool = _positive(2 * width, 2, page, D, g)
+    table = torch.arange(2 * width, dtype=torch.int32).view(2, width).cuda()
+    side = torch.cuda.Stream()
+    runs = []
+    for i in range(2):
+        q, k, v = [torch.randn((2, 1, h, D), generator=g).bfloat16().cuda() for h in (H, 2, 2)]
+        lens = _i32([n, n - 100 * i]).cuda()
+        cache = _cache(pool)
+
+        def step():
+            side.wait_stream(torch.cuda.current_stream())
+            si.cache_append(cache, k, v, table, lens, stream=side)
+            out = si.cache_attention(q, cache, table, lens + 1, stream=side)
+            torch.cuda.current_stream().wait_stream(side)
+            return out
+
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            out = step()
+        runs.append((graph, out, cache, q, lens, (k, v)))
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, run in zip(streams, runs):
+            with torch.cuda.stream(s):
+                run[0].replay()
+    torch.cuda.synchronize()
+    for _, out, cache, q, lens, _ in runs:
+        now = [t.cpu() for t in (cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale)]
+        want = kv_bounds.cache_attention(q.cpu(), *now, table.cpu(), lens.cpu() + 1)
+        kv_bounds.check(*out, want, sharp=None)
+    assert si.device_status() == si.SI_OK
