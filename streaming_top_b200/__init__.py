@@ -366,6 +366,13 @@ def _float_dtype(name, t):
     return dt
 
 
+def _fits_int(**values):
+    """ctypes would wrap an integer that a C int does not hold."""
+    for name, v in values.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name} must fit in 32 bits (got {v})")
+
+
 def _enqueue(where, device, stream, call):
     """call(stream pointer) on `stream`, or on the current stream of the
     device, with that device current for the launches."""
@@ -468,6 +475,7 @@ def cache_attention(q, cache: PagedCache, table, lens, *, window: int = 0, n_sin
     if _away(stream):
         return _elsewhere(stream, cache_attention, q, cache, table, lens, window=window, n_sink=n_sink, scale=scale,
                           out=out, lse=lse, workspace=workspace, device_status=device_status)
+    _fits_int(window=window, n_sink=n_sink)
     if q.dim() != 4 or table.dim() != 2:
         raise ValueError("q [B, L, H, D] and table [B, max_pages] expected")
     B, L, H, D = q.shape
@@ -500,6 +508,7 @@ def window_attention(q, k, v, *, window: int, n_sink: int = 0, lens=None, scale:
     if _away(stream):
         return _elsewhere(stream, window_attention, q, k, v, window=window, n_sink=n_sink, lens=lens, scale=scale,
                           out=out, lse=lse, device_status=device_status)
+    _fits_int(window=window, n_sink=n_sink)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q [B, S, H, D] and k, v [B, S, H_kv, D] expected")
     B, S, H, D = q.shape
