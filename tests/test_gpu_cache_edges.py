@@ -421,3 +421,86 @@ def test_captured_calls_on_a_side_stream():
         want = kv_bounds.cache_attention(q.cpu(), *now, table.cpu(), lens.cpu() + 1)
         kv_bounds.check(*out, want, sharp=None)
     assert si.device_status() == si.SI_OK
+
+
+# ------------------------------------------------------------------ sizes that a server meets beside decoding
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("L,H,G,D,page,window,n_sink", [
+    (300, 8, 2, 64, 16, 0, 0),      # a part of a prompt over a cached prefix
+    (300, 8, 2, 64, 16, 100, 5),
+    (130, 6, 1, 128, 128, 33, 0),   # more than a tile of queries, three rows of heads a tile's edge
+    (17, 5, 5, 128, 32, 0, 0),
+])
+def test_cache_attention_of_many_queries(dtype, L, H, G, D, page, window, n_sink):
+    """More queries than drafted tokens, sequences shorter than they are, the first of them at the start."""
+    g = _gen(L)
+    lens = [L, 700, L - 7, 3, 0]
+    need = [-(-n // page) for n in lens]
+    pool = _positive(sum(need) + 1, G, page, D, g)
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32)
+    for b, part in enumerate(torch.randperm(sum(need), generator=g).int().split(need)):
+        table[b, : need[b]] = part
+    q = (torch.randn((len(lens), L, H, D), generator=g) * 0.5).to(dtype)
+    _check_cache(q, pool, table, _i32(lens), window=window, n_sink=n_sink)
+
+
+def test_cache_attention_key_that_is_nan_reaches_only_those_who_see_it():
+    g = _gen(80)
+    page, D, H, L, n = 16, 64, 4, 5, 90
+    pool = _positive(6, 1, page, D, g)
+    table = torch.arange(6, dtype=torch.int32)[None]
+    q = (torch.randn((1, L, H, D), generator=g) * 0.5).bfloat16().cuda()
+    lens = _i32([n]).cuda()
+    for window, at, who in ((0, n - 3, [2, 3, 4]), (20, n - 22, [0, 1, 2])):
+        want = si.cache_attention(q, _cache(pool), table.cuda(), lens, window=window)
+        bad = pool[0].clone()
+        bad[at // page, 0, at % page, 7] = 0xFF
+        out, lse = si.cache_attention(q, _cache([bad, *pool[1:]]), table.cuda(), lens, window=window)
+        for i in range(L):
+            if i in who:
+                assert torch.isnan(out[0, i]).all() and torch.isnan(lse[0, i]).all()
+            else:
+                assert torch.equal(out[0, i], want[0][0, i]) and torch.equal(lse[0, i], want[1][0, i])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,G,window,n_sink", [(8, 1, 128, 4), (6, 2, 250, 0), (4, 4, 350, 30), (16, 1, 600, 3), (3, 1, 900, 0)])
+def test_window_attention_to_its_bounds(dtype, D, H, G, window, n_sink):
+    """The narrow form and both tile sizes, padded: outputs whose sums do not cancel."""
+    g = _gen(window)
+    q, k, v = [torch.randn((2, 800, n, D), generator=g) for n in (H, G, G)]
+    _check_window(q.to(dtype), k.to(dtype), (v.abs() + 0.1).to(dtype), window, n_sink, _i32([800, 611]))
+
+
+def test_chunks_of_a_prompt_equal_the_whole():
+    """A prompt through the window at once, and in parts through the cache: the
+    same where the cache holds the values exactly."""
+    g = _gen(81)
+    S, H, G, D, page, W, K = 400, 8, 2, 128, 32, 90, 4
+    code = torch.randint(0, 256, (2, 1, S, G, D), generator=g, dtype=torch.int16)
+    code = torch.where(code % 128 > 0x50, code - 0x38, code).to(torch.uint8)
+    k, v = [c.view(torch.float8_e4m3fn).bfloat16().cuda() for c in code]
+    # (one magnitude of 448 in each page and head fixes its scale at 1)
+    k[:, ::page, :, 0] = v[:, ::page, :, 1] = 448.0
+    q = (torch.randn((1, S, H, D), generator=g) * 0.02).bfloat16().cuda()
+    want = kv_bounds.window_attention(q.cpu(), k.cpu(), v.cpu(), W, K)
+    kv_bounds.check(*si.window_attention(q, k, v, window=W, n_sink=K), want, sharp=None)
+    n = -(-S // page)
+    pool = [torch.zeros((n, G, page, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pool += [torch.zeros((n, G), device="cuda") for _ in range(2)]
+    cache, table = si.PagedCache(*pool), torch.arange(n, dtype=torch.int32, device="cuda")[None]
+    done = 0
+    for part in (32, 1, 95, 2, 126, 144):  # (the parts that begin a page bring its 448)
+        lens = _i32([done]).cuda()
+        rows = slice(done, done + part)
+        si.cache_append(cache, k[:, rows].contiguous(), v[:, rows].contiguous(), table, lens)
+        out, lse = si.cache_attention(q[:, rows].contiguous(), cache, table, lens + part, window=W, n_sink=K)
+        see = kv_bounds.visible(torch.arange(done, done + part)[:, None], torch.arange(done + part), W, K)
+        ref = kv_bounds.attend(q[0, rows].cpu(), k[0, : done + part].cpu(), v[0, : done + part].cpu(), see, D ** -0.5,
+                               *kv_bounds.CACHE[torch.bfloat16], 2.0 ** -8, torch.ones(done + part, G))
+        kv_bounds.check(out[0], lse[0], ref, sharp=None)
+        done += part
+    assert done == S and pool[2].eq(1).all() and pool[3].eq(1).all()
