@@ -261,8 +261,8 @@ struct CacheCtrl {
   alignas(16) int out[2][R];          // its row of the output
   alignas(16) float red[2][R][4];     // per row and quadrant of lanes: the tile's maximum
   alignas(16) float sum[R][4];        // the same: the unit's sum
-  alignas(16) float2 ab[2][R];        // per row: factors of the state and of the tile's O
-  alignas(16) float4 col[4 * Sh::WG][Sh::HC];   // per warp and row: the tile's maximum, factors of the state and of the tile
+  alignas(16) float fa[2][R], fb[2][R];  // per row: factors of the state and of the tile's O
+  alignas(16) float col[4 * Sh::WG][3][Sh::HC];  // per warp: its rows' maxima in the tile, factors of the state, of the tile
   uint16_t nan_bits[2][C_TILE][D / 16];  // dims whose value is NaN, for tokens that only some rows see
   int nan_tok[2][8], nan_tile[2];     // first tokens of such a tile's pages, and its number
   long long scan[Sh::THREADS / 32];
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
     const int page_of = me / p.page;
     float m = ninf;  // lane c: running maximum of row c0 + c
     float l[HC], acc[HC];
-    float4* col = C->col[warp - 4];
+    float(*col)[HC] = C->col[warp - 4];
     uint32_t n_unit = 0, n_x = 0;
 
     // the softmax warps meet (bounded)
@@ -712,7 +712,12 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
 #pragma unroll
       for (int i = 1; i < TERMS; ++i)
 #pragma unroll
-        for (int c = 0; c < HC; ++c) v[c] = fmaf(t[i - 1][c], i == 1 ? 1.f / TERM_UP : 1.f / (TERM_UP * TERM_UP), v[c]);
+        for (int c = 0; c < HC; c += 2) {
+          const float f = i == 1 ? 1.f / TERM_UP : 1.f / (TERM_UP * TERM_UP);
+          const float2 x = fma2(make_float2(t[i - 1][c], t[i - 1][c + 1]), make_float2(f, f), make_float2(v[c], v[c + 1]));
+          v[c] = x.x;
+          v[c + 1] = x.y;
+        }
     };
     // joins tile j's O into the state
     auto join = [&](long long j, int qb) -> bool {
@@ -726,9 +731,11 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
       float o[HC];
       load_terms(tmem + lanes + (2 + ob) * N + c0, o);
 #pragma unroll
-      for (int c = 0; c < HC; ++c) {
-        const float2 f = C->ab[ob][c0 + c];
-        acc[c] = fmaf(o[c], f.y, acc[c] * f.x);
+      for (int c = 0; c < HC; c += 2) {
+        const float2 fa = *reinterpret_cast<const float2*>(&C->fa[ob][c0 + c]), fb = *reinterpret_cast<const float2*>(&C->fb[ob][c0 + c]);
+        const float2 x = fma2(make_float2(o[c], o[c + 1]), fb, mul2(make_float2(acc[c], acc[c + 1]), fa));
+        acc[c] = x.x;
+        acc[c + 1] = x.y;
       }
       if (C->nan_tile[ob] == static_cast<int>(j) && me < D) {
         // a value that is NaN reaches the rows that see its token, in its dim
@@ -781,7 +788,12 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
       load_terms(tmem + lanes + sb * N + c0, s);
       // log2 of weight times value scale, before the mask: a row's own scale may be 0
 #pragma unroll
-      for (int c = 0; c < HC; ++c) s[c] = fmaf(s[c] * ks, C->qs[qb][c0 + c], lr);
+      for (int c = 0; c < HC; c += 2) {
+        const float2 q2 = *reinterpret_cast<const float2*>(&C->qs[qb][c0 + c]);
+        const float2 x = fma2(mul2(make_float2(s[c], s[c + 1]), make_float2(ks, ks)), q2, make_float2(lr, lr));
+        s[c] = x.x;
+        s[c + 1] = x.y;
+      }
       if (flags & F_MASK) {
         const bool there = (d.pages >> page_of) & 1;
 #pragma unroll
@@ -804,8 +816,13 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
         const bool up = mt > m;
         const float fa = up ? f : 1.f, fb = up ? 1.f : f;
         m = fmaxf(m, mt);
-        col[lane] = make_float4(mt == ninf ? 0.f : mt, fa, fb, 0.f);
-        if (quad == 0) C->ab[sb][c0 + lane] = make_float2(fa, fb * vref * (1.f / 256.f));
+        col[0][lane] = mt == ninf ? 0.f : -mt;
+        col[1][lane] = fa;
+        col[2][lane] = fb;
+        if (quad == 0) {
+          C->fa[sb][c0 + lane] = fa;
+          C->fb[sb][c0 + lane] = fb * vref * (1.f / 256.f);
+        }
       }
       __syncwarp();
       const float ilr = __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(lr)) << 23);  // 2^-lr: the sum is of weights alone
@@ -813,15 +830,20 @@ __global__ void __launch_bounds__((CacheShape<D, R, HALF>::THREADS), (CacheShape
       // contiguous along N in groups of 16
 #pragma unroll
       for (int c = 0; c < HC; c += 4) {
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 k = col[c + i];
-          const float e = ex2(s[c + i] - k.x);
-          l[c + i] = fmaf(e * ilr, k.z, l[c + i] * k.y);
-          v[i] = e * rv;
-        }
-        __half2 x = __floats2half2_rn(v[0], v[1]), y = __floats2half2_rn(v[2], v[3]);
+        const float4 mt = *reinterpret_cast<const float4*>(&col[0][c]), fa = *reinterpret_cast<const float4*>(&col[1][c]),
+                     fb = *reinterpret_cast<const float4*>(&col[2][c]);
+        // two rows at once
+        auto pair = [&](int i, float2 m2, float2 a2, float2 b2) -> __half2 {
+          float2 e = add2(make_float2(s[c + i], s[c + i + 1]), m2);
+          e = make_float2(ex2(e.x), ex2(e.y));
+          const float2 n = fma2(mul2(e, make_float2(ilr, ilr)), b2, mul2(make_float2(l[c + i], l[c + i + 1]), a2));
+          l[c + i] = n.x;
+          l[c + i + 1] = n.y;
+          const float2 v = mul2(e, make_float2(rv, rv));
+          return __floats2half2_rn(v.x, v.y);
+        };
+        __half2 x = pair(0, make_float2(mt.x, mt.y), make_float2(fa.x, fa.y), make_float2(fb.x, fb.y));
+        __half2 y = pair(2, make_float2(mt.z, mt.w), make_float2(fa.z, fa.w), make_float2(fb.z, fb.w));
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
           const uint32_t qx = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
