@@ -165,10 +165,12 @@ def _elsewhere(stream, call, *args, **kw):
     for t in used:
         if t.get_device() != stream.device_index:
             raise ValueError(f"stream is one of {stream.device}, a tensor is on {t.device}")
-    with torch.cuda.stream(stream):
-        result = call(*args, **kw)
-    for t in used:
-        t.record_stream(stream)
+    try:
+        with torch.cuda.stream(stream):
+            result = call(*args, **kw)
+    finally:
+        for t in used:
+            t.record_stream(stream)
     for t in _tensors(result if isinstance(result, tuple) else (result,)):
         t.record_stream(here)
     return result
@@ -249,7 +251,7 @@ def indexer_topk(q, kc, w, m: int, k: int, *, q_scale=None, kc_scale=None, query
     [B,T,D/32] E8M0), kc holds MXFP4 codes [B,T,D/2] (uint8) and q is bf16.
     device_status: optional zeroed int32 CUDA tensor (>= 2 elements), this
     call's own device error word."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, indexer_topk, q, kc, w, m, k, q_scale=q_scale, kc_scale=kc_scale,
                           query_chunk=query_chunk, key_tile=key_tile, out_idx=out_idx, out_score=out_score,
                           with_score=with_score, unsorted=unsorted, kc_mx_scale=kc_mx_scale, workspace=workspace,
@@ -272,7 +274,7 @@ def indexer_topk_rows(q, kc, w, m: int, k: int, row0: int, *, q_scale=None, kc_s
     """Streaming top-k for query rows row0 .. row0+R-1 (``si_indexer_topk_rows``):
     q [B, R, H_I, D] and w [B, R, H_I] hold those rows only, kc [B, T, D] all
     keys.  Returns (idx, score) of shape [B, R, k]."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, indexer_topk_rows, q, kc, w, m, k, row0, q_scale=q_scale, kc_scale=kc_scale,
                           query_chunk=query_chunk, key_tile=key_tile, out_idx=out_idx, out_score=out_score,
                           with_score=with_score, unsorted=unsorted, kc_mx_scale=kc_mx_scale, workspace=workspace,
@@ -296,7 +298,7 @@ def indexer_topk_two_stage(q, kc, w, m: int, k: int, *, block: int = 8, n_keep: 
     n_keep blocks of `block` keys by the score of their pooled (mean) key,
     then the top-k of their keys and the incomplete block's visible keys.
     Returns (idx, score) [B, S, k], ordered as indexer_topk's."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, indexer_topk_two_stage, q, kc, w, m, k, block=block, n_keep=n_keep,
                           query_chunk=query_chunk, out_idx=out_idx, out_score=out_score, workspace=workspace,
                           device_status=device_status)
@@ -318,7 +320,7 @@ def sparse_attention(q, kv, idx, *, scale: float = 0.0, out=None, lse=None, stre
     """Sparse attention over the selected latents (``si_sparse_attention``):
     q [B,S,H,Dk] bf16, kv [B,T,Dk] bf16, idx [B,S,k] int32 (-1 padding).
     Returns (out [B,S,H,Dv=512] bf16, lse [B,S,H] fp32)."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, sparse_attention, q, kv, idx, scale=scale, out=out, lse=lse,
                           device_status=device_status)
     if q.dim() != 4 or kv.dim() != 3 or idx.dim() != 3:
@@ -415,7 +417,7 @@ def cache_append(cache: PagedCache, k, v, table, lens, *, n_new=None, stream=Non
     [B, L, H_kv, D] bf16 or fp16, table [B, max_pages] int32, lens [B] int32
     (tokens held before; not changed), n_new [B] int32 (default: L each).  The
     pages must be there (cache_reserve)."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, cache_append, cache, k, v, table, lens, n_new=n_new)
     if k.dim() != 4 or table.dim() != 2:
         raise ValueError("k, v [B, L, H_kv, D] and table [B, max_pages] expected")
@@ -472,10 +474,11 @@ def cache_attention(q, cache: PagedCache, table, lens, *, window: int = 0, n_sin
     tokens and the first `n_sink`.  Returns (out [B, L, H, D], lse [B, L, H]
     fp32).  workspace: optional scratch of
     cache_attention_workspace_size() bytes."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, cache_attention, q, cache, table, lens, window=window, n_sink=n_sink, scale=scale,
                           out=out, lse=lse, workspace=workspace, device_status=device_status)
-    _fits_int(window=window, n_sink=n_sink)
+    if (window | n_sink) >> 31:
+        _fits_int(window=window, n_sink=n_sink)
     if q.dim() != 4 or table.dim() != 2:
         raise ValueError("q [B, L, H, D] and table [B, max_pages] expected")
     B, L, H, D = q.shape
@@ -505,10 +508,11 @@ def window_attention(q, k, v, *, window: int, n_sink: int = 0, lens=None, scale:
     (``si_window_attention``): q [B, S, H, D], k and v [B, S, H_kv, D], bf16 or
     fp16; lens [B] int32 (default: S each), the rest is padding.  Returns
     (out [B, S, H, D], lse [B, S, H] fp32); padded rows give 0 and -inf."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, window_attention, q, k, v, window=window, n_sink=n_sink, lens=lens, scale=scale,
                           out=out, lse=lse, device_status=device_status)
-    _fits_int(window=window, n_sink=n_sink)
+    if (window | n_sink) >> 31:
+        _fits_int(window=window, n_sink=n_sink)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q [B, S, H, D] and k, v [B, S, H_kv, D] expected")
     B, S, H, D = q.shape
@@ -543,7 +547,7 @@ def cache_reserve(cache: PagedCache, table, lens, refs, n_new, *, status=None, s
     (``si_cache_reserve``): table [n_seq, max_pages], lens [n_seq], refs
     [n_pages], n_new [n_seq] int32; table and refs are updated.  Returns
     status [n_seq] int32: 0 done, 1 too few free pages, 2 more than max_pages."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, cache_reserve, cache, table, lens, refs, n_new, status=status)
     n_seq, max_pages = _sequence_state(cache, table, lens, refs)
     _need("n_new", n_new, torch.int32, cache.device, (n_seq,))
@@ -562,7 +566,7 @@ def cache_fork(cache: PagedCache, table, lens, refs, src, dst, *, share: bool = 
     full pages (share) or copying all of them; table, lens and refs are
     updated.  Returns status [n] int32: 0 done, 1 too few free pages, 2 not
     possible (an index out of range, dst not empty or named twice)."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, cache_fork, cache, table, lens, refs, src, dst, share=share, status=status)
     n_seq, max_pages = _sequence_state(cache, table, lens, refs)
     n = src.numel()
@@ -580,7 +584,7 @@ def cache_fork(cache: PagedCache, table, lens, refs, src, dst, *, share: bool = 
 
 def cache_free(cache: PagedCache, table, lens, refs, rows, *, stream=None):
     """Frees the sequences of the given rows (``si_cache_free``): table, lens and refs are updated."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, cache_free, cache, table, lens, refs, rows)
     n_seq, max_pages = _sequence_state(cache, table, lens, refs)
     n = rows.numel()
@@ -593,7 +597,7 @@ def cache_compact(cache: PagedCache, table, refs, *, used=None, moved=None, stre
     """Moves the pages in use together (``si_cache_compact``); table and refs
     are updated.  Returns (used [1] int32, the number of pages in use; moved
     [n_pages] int32, each used page's new place, -1 for the others)."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, cache_compact, cache, table, refs, used=used, moved=moved)
     n_seq, max_pages = _sequence_state(cache, table, None, refs)
     if used is None:
@@ -612,7 +616,7 @@ def cache_compact(cache: PagedCache, table, refs, *, used=None, moved=None, stre
 def mxfp4_to_bf16(codes, scales, out=None, stream=None):
     """Decode MXFP4 rows (``si_mxfp4_to_bf16``): codes uint8 [..., D/2], E8M0
     scales uint8 [..., D/32]; returns bf16 [..., D]."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, mxfp4_to_bf16, codes, scales, out)
     if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise ValueError("codes and scales must be uint8")
@@ -633,7 +637,7 @@ def mxfp4_to_bf16(codes, scales, out=None, stream=None):
 def sort_topk_rows(idx, score, stream=None):
     """Sort every row of (idx [..., k] int32, score [..., k] fp32) in place by
     score descending, index ascending (``si_sort_topk_rows``)."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, sort_topk_rows, idx, score)
     if idx.shape != score.shape or idx.dtype != torch.int32 or score.dtype != torch.float32:
         raise ValueError("idx int32 and score float32 of the same shape expected")
@@ -650,7 +654,7 @@ def sort_topk_rows(idx, score, stream=None):
 def indexer_materialize(q, kc, w, m: int, k: int, *, out_idx=None, out_score=None,
                         with_score: bool = True, workspace=None, stream=None):
     """Materialize-path ground truth (``si_indexer_materialize``)."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, indexer_materialize, q, kc, w, m, k, out_idx=out_idx, out_score=out_score,
                           with_score=with_score, workspace=workspace)
     B, S, T, H, D = _shapes(q, kc, w)
@@ -670,7 +674,7 @@ def indexer_materialize_noalloc(q, kc, w, m: int, k: int, *, out_idx=None, out_s
     its scratch is the library's fixed device array of NOALLOC_SCRATCH_BYTES.
     For callers that may not allocate device memory during the call; pass
     preallocated outputs to keep the call itself allocation-free."""
-    if _away(stream):
+    if stream is not None and _away(stream):
         return _elsewhere(stream, indexer_materialize_noalloc, q, kc, w, m, k, out_idx=out_idx, out_score=out_score,
                           with_score=with_score)
     B, S, T, H, D = _shapes(q, kc, w)
