@@ -504,3 +504,45 @@ def test_chunks_of_a_prompt_equal_the_whole():
         kv_bounds.check(out[0], lse[0], ref, sharp=None)
         done += part
     assert done == S and pool[2].eq(1).all() and pool[3].eq(1).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D,page,H,L,window", [
+    (64, 16, 2, 4, 0), (128, 16, 4, 4, 50), (64, 32, 8, 4, 60), (128, 64, 16, 4, 0), (64, 128, 128, 2, 200), (128, 16, 5, 40, 20)])
+def test_cache_attention_values_that_are_nan(dtype, D, page, H, L, window):
+    """NaN values of tokens that some queries see and others do not, for all
+    numbers of rows: NaN in those rows' dims, and nothing else changes."""
+    g = _gen(D + H)
+    n = 300
+    n_pages = -(-n // page)
+    pool = _positive(n_pages, 1, page, D, g)
+    table = torch.randperm(n_pages, generator=g).int()[None]
+    q = (torch.randn((1, L, H, D), generator=g) * 0.5).to(dtype).cuda()
+    lens = _i32([n]).cuda()
+    want = si.cache_attention(q, _cache(pool), table.cuda(), lens, window=window)
+    bad = pool[1].clone()
+    first = n - L - window + 1 if window else n - L - 5  # (the first query's window begins there)
+    where = [(first + i, (13 * i) % D) for i in (-1, 0, 1, 2)] + [(n - 2, 1), (n - 2, D - 1), (n - 1, 16), (n - L, 17)]
+    for t, d in where:
+        bad[table[0, t // page], 0, t % page, d] = 0x7F if t % 2 else 0xFF
+    out, lse = si.cache_attention(q, _cache([pool[0], bad, *pool[2:]]), table.cuda(), lens, window=window)
+    assert torch.equal(lse, want[1])
+    for i in range(L):
+        p = n - L + i
+        dims = sorted({d for t, d in where if t <= p and (not window or t > p - window)})
+        keep = [d for d in range(D) if d not in dims]
+        assert torch.isnan(out[0, i][:, dims]).all()
+        assert torch.equal(out[0, i][:, keep], want[0][0, i][:, keep])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_the_most_heads_that_share_one(dtype):
+    """128 query heads on one, through both attentions."""
+    g = _gen(90)
+    q, k, v = [torch.randn((1, 300, n, 64), generator=g) for n in (128, 1, 1)]
+    for window, n_sink in ((100, 3), (280, 0)):
+        _check_window(q[:, :150].to(dtype).contiguous(), k[:, :150].to(dtype).contiguous(),
+                      (v.abs() + 0.1)[:, :150].to(dtype).contiguous(), window, n_sink)
+    pool = _positive(40, 1, 32, 64, g)
+    table = torch.arange(40, dtype=torch.int32)[None]
+    _check_cache((q[:, :2] * 0.5).to(dtype).contiguous(), pool, table, _i32([1270]), window=0)
