@@ -233,7 +233,8 @@ __device__ __noinline__ void row_by_keys(const WindowParams& p, const Item& it, 
     for (int d = 0; d < N; ++d) s = fmaf(q[d], load16<HALF>(p.k, at + d * 32 + lane), s);
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
     s *= p.scale_log2;
-    const float mn = fmaxf(m, s), c = m == mn ? 1.f : ex2(m - mn), e = s == mn ? 1.f : ex2(s - mn);
+    // as by tiles: scores of -infinity weigh nothing, of +infinity NaN
+    const float mn = fmaxf(m, s), off = mn == -INFINITY ? 0.f : mn, c = ex2(m - off), e = ex2(s - off);
     m = mn;
     sum = fmaf(sum, c, e);
     for (int d = 0; d < N; ++d) acc[d] = fmaf(e, load16<HALF>(p.v, at + d * 32 + lane), acc[d] * c);

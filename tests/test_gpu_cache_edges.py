@@ -546,3 +546,32 @@ def test_the_most_heads_that_share_one(dtype):
     pool = _positive(40, 1, 32, 64, g)
     table = torch.arange(40, dtype=torch.int32)[None]
     _check_cache((q[:, :2] * 0.5).to(dtype).contiguous(), pool, table, _i32([1270]), window=0)
+
+
+@pytest.mark.parametrize("window", [40, 300])
+@pytest.mark.parametrize("by_keys", [False, True])
+def test_window_attention_scores_that_are_infinite(window, by_keys):
+    """A key with an infinity: rows whose score with it is +infinity give NaN,
+    those with -infinity do not count it, also in blocks done key by key."""
+    g = _gen(91)
+    S, at = 500, 100
+    q, k, v = [torch.randn((1, S, n, 128), generator=g).bfloat16() for n in (2, 1, 1)]
+    q[..., 5] = torch.where(torch.arange(S) % 2 == 0, 1.0, -1.0)[None, :, None]
+    v = v.abs() + 0.1
+    pos = torch.arange(S)
+    see = kv_bounds.visible(pos[:, None], pos, window, 0)
+    sees_it = see[:, at]
+    k[0, at, 0, 5] = 0
+    want = kv_bounds.attend(q[0], k[0], v[0], see & (pos != at), 128 ** -0.5, *kv_bounds.WINDOW[torch.bfloat16], 2.0 ** -8)
+    k[0, at, 0, 5] = float("inf")
+    if by_keys:  # a value that is NaN, of the last token alone and of one far from the key
+        v[0, S - 1, 0, 3] = v[0, at + 30, 0, 3] = float("nan")
+    out, lse = [t[0].cpu() for t in si.window_attention(*_cuda(q, k, v), window=window)]
+    up = sees_it & (pos % 2 == 0)
+    assert torch.isnan(out[up]).all() and torch.isnan(lse[up]).all()
+    rest = ~up
+    if by_keys:
+        touched = see[:, at + 30] | (pos == S - 1)
+        assert torch.isnan(out[touched][..., 3]).all()
+        out[touched] = torch.where(torch.arange(128) == 3, want[0][touched].bfloat16(), out[touched])
+    kv_bounds.check(out[rest], lse[rest], [t[rest] for t in want])
