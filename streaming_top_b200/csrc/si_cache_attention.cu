@@ -35,14 +35,15 @@
 // second kernel is launched.
 //
 // Measured (D = 128 unless said; bytes are those of the visible codes): 64
-// sequences of 4096 to 8192 tokens, 64 / 8 heads: 150 us, 5.4 TB/s of 6.5; 16
-// of 8192 to 16,384 tokens, four queries each, 32 / 8 heads, D = 64, fp16: 115 us,
-// 1.8 TB/s; one of 262,143 tokens, 64 / 1 heads: 78 us, 0.86 TB/s; windows of 128
-// tokens and 4 sinks in 128 sequences: 33 us.  With eight rows a head a tile
-// takes 2700 clocks in each of an SM's two CTAs, near the 1400 that its bytes
-// need; with more rows, or few tiles a CTA, the hand-offs between the warps (a
-// tile's S, maximum, P, O) are what is left: without the exponentials, the
-// rounding to terms and the maxima, 64 rows take 93 instead of 98 us.
+// sequences of 4096 to 8192 tokens, 64 / 8 heads: 150 to 160 us from one GPU to
+// another, 5.4 to 5.1 TB/s of 6.5; 16 of 8192 to 16,384 tokens, four queries each,
+// 32 / 8 heads, D = 64, fp16: 111 us, 1.9 TB/s; one of 262,143 tokens, 64 / 1 heads:
+// 75 us, 0.89 TB/s; windows of 128 tokens and 4 sinks in 128 sequences: 33 us.
+// With eight rows a head a tile takes 2700 clocks in each of an SM's two CTAs, near
+// the 1400 that its bytes need; with more rows, or few tiles a CTA, the hand-offs
+// between the warps (a tile's S, maximum, P, O) are what is left.  The joining
+// kernel takes some 20 of the 75 us of the long sequence (64 of its blocks work,
+// each on 148 partial results in turn), 8 of the 150 and of the 111.
 //
 // Warps: 0 schedules (walks the tiles, reads page table and scales ahead,
 // publishes tile descriptors) and loads pages by TMA; 1 issues the MMAs; 2-3

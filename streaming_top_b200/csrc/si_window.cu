@@ -17,7 +17,11 @@
 // the band's first key.  Per key tile and query tile:
 //   S = Q K^T      tcgen05 kind::f16, M = 128 rows, N = KT keys, into TMEM
 //   softmax        a thread a row: running maximum and sum in registers, P
-//                  rounded to the inputs' type over S in TMEM
+//                  rounded to the inputs' type over S in TMEM (the product takes
+//                  operands of one type; the sum is of the unrounded weights:
+//                  0.0023 of the outputs' size off in bf16, 0.0016 by their own
+//                  rounding; fp16 0.00026 and 0.00020.  A second product with
+//                  what the rounding leaves would double the PV time)
 //   O += P V       A = P from TMEM, B = V read along dims (MN-major)
 // O stays in TMEM; it is rescaled only when a row's maximum grows by more than
 // 2^8 (P is then at most 256), which after the first tiles hardly happens.
@@ -746,13 +750,15 @@ __global__ void __launch_bounds__(W_THREADS, 1)
 // softmax, V's during the next QK.
 //
 // Window 128, 4 sinks, 64 query and 8 key/value heads, D = 128, 16,384
-// positions: 188 us (3.2 TB/s of 6.5, 22 % of the bf16 rate); the streaming
-// form 276 us.  What is left is latency: a query tile's QK, softmax, PV and
-// epilogue follow one another (1.3, 4, 1.4 and 2.7 thousand clocks), and with
+// positions: 186 to 193 us from one GPU to another (3.3 to 3.2 TB/s of 6.5, 24 %
+// of the bf16 rate), 171 us where calls in a row leave their inputs in L2; the
+// streaming form 276 us.  What is left is latency: a query tile's QK, softmax, PV
+// and epilogue follow one another (1.3, 4, 1.4 and 2.7 thousand clocks), and with
 // O over S only two fit into tensor memory.  Without the stores it takes 34 us
-// less, without the exponentials 18.  Tried and not faster: two warpgroups a
-// query tile that share its columns (232 us) or take items in turn (194 us),
-// a share of the exponentials on the FMA units (177 to 194 against 177 us).
+// less, without the exponentials 18.  Tried and not faster, each against this
+// form in the same run: two warpgroups a query tile that share its columns (232
+// to 193 us) or take items in turn (194 to 193), a share of the exponentials on
+// the FMA units (177 to 194 against 177, inputs in L2).
 
 struct BandItem {
   int b, h, p0, len, k_start, sink_end;
@@ -822,7 +828,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = C->tmem_slot;
   // items of this CTA, all with the same steps (padding's too: skipping it cost
-  // the others 9 %, 197 against 180 us): number i waits for parity i & 1
+  // the others 9 %, 197 against 180 us in one run): number i waits for parity i & 1
 
   if (warp == 0) {
     if (lane == 0) {
